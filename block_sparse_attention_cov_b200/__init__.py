@@ -11,9 +11,19 @@ CPU path. The names mirror the C calls:
     forward_host(q_h, k_h, v_h, beta, out_h, ...)  # solattn_forward_host (host tensors)
 
 q, k, v: CUDA bf16 tensors [B, H, N, d], contiguous, d in {64, 128}.
+
+Around attention (_rotary.py, _cache.py):
+
+    rope = Rotary(d, layout="interleaved", sections=(t, h, w))
+    q, k = rotary(q, k, rope, positions)           # solattn_rotary
+    q, k, stats = rotary_pool(q, k, v, rope, positions)   # solattn_rotary_pool: rotary + pool
+    cache = Cache.empty(pages, heads, d)
+    cache_append(cache, k, v, table, lengths)      # solattn_cache_append
+    out, lse = cache_attention(q, cache, table, lengths)  # solattn_cache_attention
 """
 from __future__ import annotations
 
+import contextlib
 import ctypes
 import math
 from dataclasses import dataclass
@@ -23,7 +33,8 @@ import torch
 from . import _lib
 
 __all__ = ["SolAttnError", "PooledStats", "pool", "forward", "dense", "status", "workspace", "pooled_bytes",
-           "host_scratch", "forward_host"]
+           "host_scratch", "forward_host", "Rotary", "rotary", "rotary_pool", "Cache", "cache_append",
+           "cache_workspace", "cache_attention"]
 
 
 class SolAttnError(RuntimeError):
@@ -72,6 +83,42 @@ def _ptr(t):
     return None if t is None else ctypes.c_void_p(t.data_ptr())
 
 
+def _tensor_strides(t):
+    """solattn_strides_t of one [B, H, N, d] tensor; a dimension of one element has no stride that matters."""
+    if t.is_contiguous():
+        return _lib.StridesStruct(0, 0, 0)
+    B, H, N, _ = t.shape
+    sb, sh, sn, _ = t.stride()
+    st = _lib.StridesStruct(sb if B > 1 else 0, sh if H > 1 else 0, sn if N > 1 else 0)
+    if B * H * N > 1 and st.batch == st.head == st.token == 0:
+        raise ValueError("a tensor of one repeated row (expand()) is not supported")
+    return st
+
+
+def _dtype(t, fp32: bool) -> int:
+    codes = {torch.bfloat16: _lib.BF16, torch.float16: _lib.F16}
+    if fp32:
+        codes[torch.float32] = _lib.F32
+    if t.dtype not in codes:
+        raise ValueError(f"unsupported type {t.dtype}")
+    return codes[t.dtype]
+
+
+def _same_device(*ts):
+    ts = [t for t in ts if t is not None]
+    if not all(t.is_cuda and t.device == ts[0].device for t in ts):
+        raise ValueError("all tensors must be on one CUDA device")
+
+
+def _current(t):
+    """The tensor's device as the current one for a call (nothing to do where it is already)."""
+    return contextlib.nullcontext() if t.device.index == torch.cuda.current_device() else torch.cuda.device(t.device)
+
+
+def _stream_on(t) -> ctypes.c_void_p:
+    return ctypes.c_void_p(torch.cuda.current_stream(t.device).cuda_stream)
+
+
 def pooled_bytes(B: int, H: int, N: int, d: int) -> int:
     n = ctypes.c_size_t(0)
     _check(_lib.lib().solattn_pooled_layout(B, H, N, d, None, None, ctypes.byref(n)), "solattn_pooled_layout")
@@ -99,9 +146,8 @@ class PooledStats:
         return self.buffer[off:off + size * n].view(dt).view(dims)
 
 
-def pool(q: torch.Tensor, k: torch.Tensor, v: torch.Tensor, stats: PooledStats | None = None) -> PooledStats:
-    """Block means of q, k, v and the mean and covariance of the pooled keys (solattn_pool)."""
-    _check_inputs(q, k, v)
+def _pooled_stats(q: torch.Tensor, stats: PooledStats | None) -> PooledStats:
+    """`stats` checked against q's shape, or newly allocated ones."""
     B, H, N, d = _shape(q)
     if stats is None:
         nbytes = pooled_bytes(B, H, N, d)
@@ -112,6 +158,14 @@ def pool(q: torch.Tensor, k: torch.Tensor, v: torch.Tensor, stats: PooledStats |
         stats = PooledStats(buf, st, (B, H, N, d))
     elif stats.shape != (B, H, N, d):
         raise ValueError("PooledStats shape does not match the inputs")
+    return stats
+
+
+def pool(q: torch.Tensor, k: torch.Tensor, v: torch.Tensor, stats: PooledStats | None = None) -> PooledStats:
+    """Block means of q, k, v and the mean and covariance of the pooled keys (solattn_pool)."""
+    _check_inputs(q, k, v)
+    B, H, N, d = _shape(q)
+    stats = _pooled_stats(q, stats)
     if q.is_contiguous():
         _check(_lib.lib().solattn_pool(_ptr(q), _ptr(k), _ptr(v), B, H, N, d, ctypes.byref(stats.struct),
                                        _stream()), "solattn_pool")
@@ -233,3 +287,7 @@ def status(ws: torch.Tensor) -> int:
     """Synchronises the current stream and returns the device status of the last
     call that used `ws` (0 = ok, 5 = a bounded wait expired)."""
     return int(_lib.lib().solattn_status(_ptr(ws), _stream()))
+
+
+from ._cache import Cache, cache_append, cache_attention, cache_workspace  # noqa: E402
+from ._rotary import Rotary, rotary, rotary_pool  # noqa: E402

@@ -17,8 +17,9 @@ LIB = os.path.join(PKG, "libsolattn.so")
 # Test-only variant (failure-detection tests): adds solattn_test_set_hook, which
 # makes one CTA skip its first K tile and shortens the bounded-wait budget.
 LIB_HOOKS = os.path.join(PKG, "libsolattn_testhooks.so")
-SOURCES = ["api.cu", "pool.cu", "forward.cu", "forward_pp.cu"]
-HEADERS = ["kernels.h", "ptx.cuh", "fwd_common.cuh"]
+SOURCES = ["api.cu", "ops_api.cu", "pool.cu", "forward.cu", "forward_pp.cu", "rotary.cu", "cache_append.cu",
+           "cache_step.cu", "cache_chunk.cu"]
+HEADERS = ["kernels.h", "api_common.h", "ptx.cuh", "fwd_common.cuh", "cache_common.cuh"]
 
 NVCC_FLAGS = [
     "-gencode", "arch=compute_100a,code=sm_100a",

@@ -7,28 +7,17 @@
 #include <mutex>
 
 #include "../../include/solattn.h"
+#include "api_common.h"
 #include "kernels.h"
 #include "ptx.cuh"
 
-namespace {
+// Shared with ops_api.cu (api_common.h).
+namespace solattn {
 
-#ifdef SOLATTN_TEST_HOOKS
-bool g_force_one_unit = false;  // test builds: run every forward on the one-unit kernel
-#endif
-
-using solattn::DeviceStatus;
-using solattn::PooledPtrs;
-
-static_assert(sizeof(DeviceStatus) <= SOLATTN_WORKSPACE_BYTES, "workspace too small for the status block");
-
-constexpr int kMaxDevices = 64;
 // Multiprocessor count per device: 0 = not yet queried, -1 = not an sm_100
 // device. Filled lazily; concurrent first calls may both query the device and
 // store the same value, which the atomic makes well defined.
-std::atomic<int> g_sms[kMaxDevices];
-
-bool aligned16(const void* p) { return (reinterpret_cast<uintptr_t>(p) & 15u) == 0; }
-bool aligned4(const void* p) { return (reinterpret_cast<uintptr_t>(p) & 3u) == 0; }
+static std::atomic<int> g_sms[kMaxDevices];
 
 int check_shape(int B, int H, int N, int d) {
   if (B <= 0 || H <= 0 || N <= 0 || d <= 0) return SOLATTN_ERR_ARG;
@@ -81,17 +70,38 @@ int current_device_sms(int* sms) {
 // token stride at least d, and the head (batch) stride non-zero when there is
 // more than one head (batch): out shares these strides, and two heads writing
 // the same rows would race.
-int resolve_strides(const solattn_strides_t* in, int B, int H, int N, int d, solattn::Strides* out) {
+int resolve_strides(const solattn_strides_t* in, int B, int H, int N, int d, Strides* out) {
   if (!in || (in->batch == 0 && in->head == 0 && in->token == 0)) {
-    *out = solattn::Strides{static_cast<long long>(H) * N * d, static_cast<long long>(N) * d, d};
+    *out = Strides{static_cast<long long>(H) * N * d, static_cast<long long>(N) * d, d};
     return SOLATTN_OK;
   }
   if (in->batch < 0 || in->head < 0 || in->token < d) return SOLATTN_ERR_ARG;
   if ((H > 1 && in->head == 0) || (B > 1 && in->batch == 0)) return SOLATTN_ERR_ARG;
   if ((in->batch | in->head | in->token) & 7) return SOLATTN_ERR_ARG;
-  *out = solattn::Strides{in->batch, in->head, in->token};
+  *out = Strides{in->batch, in->head, in->token};
   return SOLATTN_OK;
 }
+
+}  // namespace solattn
+
+namespace {
+
+#ifdef SOLATTN_TEST_HOOKS
+bool g_force_one_unit = false;  // test builds: run every forward on the one-unit kernel
+#endif
+
+using solattn::DeviceStatus;
+using solattn::PooledPtrs;
+using solattn::aligned16;
+using solattn::aligned4;
+using solattn::check_pooled;
+using solattn::check_qkv;
+using solattn::check_shape;
+using solattn::current_device_sms;
+using solattn::kMaxDevices;
+using solattn::resolve_strides;
+
+static_assert(sizeof(DeviceStatus) <= SOLATTN_WORKSPACE_BYTES, "workspace too small for the status block");
 
 PooledPtrs to_ptrs(const solattn_pooled_t* p) {
   return PooledPtrs{p->qbar, p->kbar, p->vbar, p->kmean, p->kcov, static_cast<uint16_t*>(p->kbar16),
@@ -195,6 +205,7 @@ const char* solattn_strerror(int code) {
     case SOLATTN_ERR_DEVICE: return "current device is not an sm_100 (B200-class) GPU";
     case SOLATTN_ERR_WORKSPACE: return "workspace missing or smaller than SOLATTN_WORKSPACE_BYTES";
     case SOLATTN_ERR_SCRATCH: return "problem too large for the static scratch of solattn_forward_noalloc";
+    case SOLATTN_ERR_PAGE: return "a page number, length or count outside the cache or its table";
     default: return "unknown status code";
   }
 }

@@ -54,6 +54,92 @@ cudaError_t launch_forward(const ForwardArgs& a, int num_sms, cudaStream_t strea
 // path.
 cudaError_t launch_forward_pp(const ForwardArgs& a, int num_sms, cudaStream_t stream);
 
+// Mean and covariance of the pooled keys (the second launch of launch_pool).
+cudaError_t launch_key_stats(const float* kbar, float* kmean, float* kcov, int BH, int NB, int d,
+                             cudaStream_t stream);
+
+enum { kBF16 = 0, kF16 = 1, kF32 = 2 };  // == solattn_dtype
+
+// Rotary positions (rotary.cu).
+struct RotaryTable {
+  const unsigned long long* freq;  // turns per unit of position, in 2^-64
+  const int32_t* axis;             // position axis of each pair; null: axis 0
+  const int32_t* pos;
+  long long pos_b, pos_n;          // strides of pos (batch, token)
+  int rot, axes, layout;           // layout 0: interleaved pairs, 1: halves
+  int inverse;
+  float gain;
+};
+struct RotaryArgs {
+  const void* x[2];  // queries, keys (x[1] null: queries only)
+  void* y[2];
+  Strides xs[2], ys[2];
+  int heads[2];
+  int dtype, B, N, d;
+  RotaryTable t;
+};
+cudaError_t launch_rotary(const RotaryArgs& a, int num_sms, cudaStream_t stream);
+
+struct RotaryPoolArgs {
+  const uint16_t* x[3];  // q, k, v
+  uint16_t* y[2];        // rotated q, k
+  float* bar[3];         // qbar, kbar, vbar
+  uint16_t* bar16[3];    // null, kbar16, vbar16
+  Strides st, ys;        // of q, k, v and of the rotated q, k
+  int B, H, N, d;
+  RotaryTable t;
+};
+cudaError_t launch_rotary_pool(const RotaryPoolArgs& a, int num_sms, cudaStream_t stream);
+
+// 8-bit cache: writing tokens (cache_append.cu).
+struct DeviceStatus;
+struct CacheAppendArgs {
+  const void* x[2];    // keys, values [B][H][N][d]
+  uint8_t* data[2];    // e4m3 pages
+  float* scale[2];
+  Strides st;          // of x
+  long long page_stride, scale_stride, table_stride;
+  const int32_t* table;
+  const int32_t* lengths;
+  const int32_t* counts;  // may be null
+  int dtype, pages, columns, B, H, N, d;
+  DeviceStatus* status;   // may be null
+};
+cudaError_t launch_cache_append(const CacheAppendArgs& a, cudaStream_t stream);
+
+// 8-bit cache: attention (cache_step.cu, cache_chunk.cu).
+struct CacheAttnArgs {
+  const uint16_t* q;
+  uint16_t* out;
+  float* lse;  // may be null
+  const uint8_t* k;
+  const uint8_t* v;
+  const float* k_scale;
+  const float* v_scale;
+  const int32_t* table;
+  const int32_t* lengths;
+  const int32_t* counts;  // may be null: N each
+  Strides st, ost;        // of q and of out
+  long long page_stride, scale_stride, table_stride;
+  float scale_log2;       // softmax scale * log2(e)
+  int dtype, pages, columns, B, H, Hk, N, d;
+  int group;              // H / Hk
+  int causal;
+  int splits;             // parts of the key axis, joined from part_o / part_ml when > 1
+  float* part_o;          // [B][H][N][splits][d]
+  float2* part_ml;        // [B][H][N][splits] (reference, sum)
+  DeviceStatus* status;
+};
+// Which kernel a call takes, and how many parts its key axis is split into.
+struct CachePlan {
+  bool step;
+  int splits;
+};
+CachePlan cache_plan(int B, int H, int Hk, int N, int columns);
+cudaError_t launch_cache_step(const CacheAttnArgs& a, cudaStream_t stream);
+cudaError_t launch_cache_chunk(const CacheAttnArgs& a, cudaStream_t stream);
+cudaError_t launch_cache_join(const CacheAttnArgs& a, cudaStream_t stream);
+
 #ifdef SOLATTN_TEST_HOOKS
 // Test builds only: hook variables of each kernel's translation unit.
 cudaError_t set_test_hooks_fwd(int skip_cta, unsigned long long wait_budget_ns);

@@ -268,6 +268,15 @@ __global__ void __cluster_dims__(kSplit, 1, 1) __launch_bounds__(256)
 }
 
 template <int D>
+cudaError_t launch_key_stats_d(const float* kbar, float* kmean, float* kcov, int BH, int NB, cudaStream_t stream) {
+  const int smem = static_cast<int>(sizeof(KeyStatsSmem<D>));
+  const cudaError_t e = cudaFuncSetAttribute(key_stats_kernel<D>, cudaFuncAttributeMaxDynamicSharedMemorySize, smem);
+  if (e != cudaSuccess) return e;
+  key_stats_kernel<D><<<dim3(kSplit, BH), 256, smem, stream>>>(kbar, kmean, kcov, NB);
+  return cudaGetLastError();
+}
+
+template <int D>
 cudaError_t launch_pool_d(const uint16_t* q, const uint16_t* k, const uint16_t* v, const PooledPtrs& p, int BH,
                           int H, int N, const Strides& st, int num_sms, cudaStream_t stream) {
   const int NB = (N + kBlock - 1) / kBlock;
@@ -275,16 +284,18 @@ cudaError_t launch_pool_d(const uint16_t* q, const uint16_t* k, const uint16_t* 
   const int grid1 = static_cast<int>(items < num_sms * 8ll ? items : num_sms * 8ll);
   pool_means_kernel<D><<<grid1, 256, 0, stream>>>(q, k, v, p.qbar, p.kbar, p.vbar, p.kbar16, p.vbar16, BH, H, N,
                                                    NB, st);
-  cudaError_t e = cudaGetLastError();
+  const cudaError_t e = cudaGetLastError();
   if (e != cudaSuccess) return e;
-  const int smem = static_cast<int>(sizeof(KeyStatsSmem<D>));
-  e = cudaFuncSetAttribute(key_stats_kernel<D>, cudaFuncAttributeMaxDynamicSharedMemorySize, smem);
-  if (e != cudaSuccess) return e;
-  key_stats_kernel<D><<<dim3(kSplit, BH), 256, smem, stream>>>(p.kbar, p.kmean, p.kcov, NB);
-  return cudaGetLastError();
+  return launch_key_stats_d<D>(p.kbar, p.kmean, p.kcov, BH, NB, stream);
 }
 
 }  // namespace
+
+cudaError_t launch_key_stats(const float* kbar, float* kmean, float* kcov, int BH, int NB, int d,
+                             cudaStream_t stream) {
+  if (d == 64) return launch_key_stats_d<64>(kbar, kmean, kcov, BH, NB, stream);
+  return launch_key_stats_d<128>(kbar, kmean, kcov, BH, NB, stream);
+}
 
 cudaError_t launch_pool(const uint16_t* q, const uint16_t* k, const uint16_t* v, const PooledPtrs& p, int BH,
                         int H, int N, int d, const Strides& st, int num_sms, cudaStream_t stream) {

@@ -55,7 +55,8 @@ enum solattn_status_code {
   SOLATTN_ERR_TIMEOUT = 5,     /* a bounded device wait expired (device side) */
   SOLATTN_ERR_DEVICE = 6,      /* current device is not an sm_100 GPU */
   SOLATTN_ERR_WORKSPACE = 7,   /* workspace missing or smaller than SOLATTN_WORKSPACE_BYTES */
-  SOLATTN_ERR_SCRATCH = 8      /* problem needs more than SOLATTN_NOALLOC_SCRATCH_BYTES of scratch */
+  SOLATTN_ERR_SCRATCH = 8,     /* problem needs more than SOLATTN_NOALLOC_SCRATCH_BYTES of scratch */
+  SOLATTN_ERR_PAGE = 9         /* a page number, length or count outside the cache (device side) */
 };
 
 /*
@@ -296,6 +297,173 @@ int solattn_host_scratch_bytes(int B, int H, int N, int d, int chunk_heads, size
 int solattn_forward_host(const void* q, const void* k, const void* v, int B, int H, int N, int d, float beta,
                          void* out, float* lse, int32_t* density_out, int chunk_heads, void* scratch,
                          size_t scratch_bytes, void* stream);
+
+/* ---------------------------------------------------------------------------
+ * Operators around attention: rotary positions on q and k (alone, or in the
+ * same pass as the pooled statistics), and a key/value cache held in 8 bits with
+ * a scale per 64-token block and head. They are general transformer operators
+ * with no counterpart on the pages; the blocks are the library's 64 tokens.
+ * ------------------------------------------------------------------------- */
+
+enum solattn_dtype {
+  SOLATTN_BF16 = 0,
+  SOLATTN_F16 = 1,
+  SOLATTN_F32 = 2
+};
+
+/*
+ * Rotary positions. Pair p of a token at position m turns by the angle m f_p and
+ * is scaled by gain:
+ *   y0 = gain (x0 cos - x1 sin),  y1 = gain (x1 cos + x0 sin),
+ * where the pairs of the first `rot` elements of a head are (2p, 2p + 1)
+ * (SOLATTN_ROTARY_INTERLEAVED) or (p, p + rot/2) (SOLATTN_ROTARY_HALF). The
+ * elements behind `rot` are copied. A pair takes its position from one of up to
+ * four axes (video: t, h, w).
+ *
+ * freq[p] is the turn per unit of position as a fraction of 2^64,
+ * round(f_p / (2 pi) 2^64): the angle is reduced exactly at every position,
+ * negative ones too. solattn_rotary_frequencies fills it.
+ */
+#define SOLATTN_ROTARY_MAX_AXES 4
+#define SOLATTN_ROTARY_MAX_DIM 1024
+enum solattn_rotary_layout {
+  SOLATTN_ROTARY_INTERLEAVED = 0,
+  SOLATTN_ROTARY_HALF = 1
+};
+typedef struct {
+  int rot;                  /* rotated leading elements of a head: even, 2 .. d */
+  int layout;               /* enum solattn_rotary_layout */
+  int axes;                 /* position axes, 1 .. SOLATTN_ROTARY_MAX_AXES */
+  float gain;               /* factor on cos and sin (1, or the scaling's) */
+  const uint64_t* freq;     /* device, [rot / 2] */
+  const int32_t* axis;      /* device, [rot / 2]: axis of each pair; NULL when axes == 1 */
+  const int32_t* positions; /* device: token (b, n), axis a at b * position_batch + n * position_token + a */
+  long long position_batch; /* 0: the batch shares its positions */
+  long long position_token; /* 0 = axes (contiguous) */
+} solattn_rotary_t;
+
+/*
+ * Host-only: frequencies f_i = theta^(-i / n) of the n pairs of each axis
+ * (pairs[axes], summing to rot / 2; NULL when axes == 1), scaled for contexts
+ * longer than those trained on, as the fractions of solattn_rotary_t, with each
+ * pair's axis (axis may be NULL when axes == 1) and the gain:
+ *   SOLATTN_SCALING_LINEAR  f / factor
+ *   SOLATTN_SCALING_NTK     theta becomes theta factor^(2n / (2n - 2))
+ *   SOLATTN_SCALING_YARN    f (keep + (1 - keep) / factor), keep = clamp((r - slow) / (fast - slow), 0, 1),
+ *                           r = original f / (2 pi) the turns within `original` tokens (usual: fast 32,
+ *                           slow 1); gain 0.1 ln(factor) + 1
+ */
+enum solattn_rotary_scaling {
+  SOLATTN_SCALING_NONE = 0,
+  SOLATTN_SCALING_LINEAR = 1,
+  SOLATTN_SCALING_NTK = 2,
+  SOLATTN_SCALING_YARN = 3
+};
+int solattn_rotary_frequencies(int rot, int axes, const int* pairs, double theta, int scaling, double factor,
+                               double original, double fast, double slow, uint64_t* freq, int32_t* axis,
+                               float* gain);
+
+/*
+ * Rotates q [B][H][N][d] and, when k != NULL, k [B][H_kv][N][d] of the same
+ * tokens into q_out and k_out, in one launch. dtype: bf16, fp16 or fp32 (sums in
+ * fp32, one rounding). d <= SOLATTN_ROTARY_MAX_DIM. Strides as in
+ * solattn_strides_t but per tensor, of any multiple of one element (NULL =
+ * contiguous; rows on 16-byte boundaries go with 16-byte accesses); an input's
+ * may be 0 (a broadcast). Pointers need the element's alignment only. In place
+ * (q_out == q with the same strides) is allowed; any other overlap is not.
+ * inverse != 0 turns by -m f_p: the transpose, so the gradient of the inputs
+ * from the gradient of the outputs.
+ */
+int solattn_rotary(const void* q, const void* k, void* q_out, void* k_out, int dtype, int B, int H, int H_kv, int N,
+                   int d, const solattn_strides_t* q_strides, const solattn_strides_t* k_strides,
+                   const solattn_strides_t* q_out_strides, const solattn_strides_t* k_out_strides,
+                   const solattn_rotary_t* rotary, int inverse, void* stream);
+
+/*
+ * solattn_rotary on bf16 q and k [B][H][N][d] and solattn_pool of the result, q,
+ * k and v being read once: writes q_out, k_out and every array of `pooled`, for
+ * solattn_forward on (q_out, k_out, v). qbar and kbar are the means of the
+ * rotated values before their rounding to bf16. rot must be d
+ * (SOLATTN_ERR_UNSUPPORTED otherwise: rotate, then pool). q, k, v share
+ * *strides, q_out and k_out share *out_strides, both under the rules of
+ * solattn_strides_t; in place is allowed as in solattn_rotary.
+ */
+int solattn_rotary_pool(const void* q, const void* k, const void* v, void* q_out, void* k_out, int B, int H, int N,
+                        int d, const solattn_strides_t* strides, const solattn_strides_t* out_strides,
+                        const solattn_rotary_t* rotary, const solattn_pooled_t* pooled, void* stream);
+
+/*
+ * Key/value cache in 8 bits. A page holds 64 tokens of every head:
+ *   k, v              e4m3 [pages][heads][64][d], d in {64, 128}
+ *   k_scale, v_scale  fp32 [pages][heads], positive
+ * and a value is e4m3 * scale. page_stride (bytes, a multiple of 16) and
+ * scale_stride (floats) are the steps between pages, 0 = contiguous. A sequence
+ * is a row of a table [B][columns]: the page of each of its 64-token blocks
+ * (table_stride entries between rows, 0 = columns). Sequences may share pages
+ * that are only read. table, lengths and counts are device memory, so a captured
+ * graph follows their contents.
+ *
+ * What the device finds out of range (a page number outside [0, pages), a
+ * length or count outside the table or the tensors) touches no memory outside
+ * the cache: tokens of such a page are not written and not attended, lengths
+ * and counts are clamped, and SOLATTN_ERR_PAGE is kept in the workspace until the
+ * caller clears its first SOLATTN_WORKSPACE_BYTES (solattn_status reads it). Those
+ * bytes are the status block: clear them once before the first use.
+ */
+#define SOLATTN_CACHE_MAX_COLUMNS (1 << 22)
+typedef struct {
+  void* k;
+  void* v;
+  float* k_scale;
+  float* v_scale;
+  int pages;
+  int heads;
+  int d;
+  long long page_stride;
+  long long scale_stride;
+} solattn_cache_t;
+
+/*
+ * Writes new tokens' keys and values: tokens 0 .. counts[b] - 1 (counts NULL: N)
+ * of k, v [B][heads][N][d] (bf16, fp16 or fp32; *strides shared, multiples of 8
+ * elements, NULL = contiguous) go to places lengths[b] .. of sequence b. The
+ * caller's lengths do not change.
+ *
+ * A page's scale is the smallest power of two with max |x| <= 448 scale, within
+ * 2^-32 .. 2^32 (larger values saturate), the maximum being over the finite
+ * elements of the page's new tokens; in a page that holds older tokens it never
+ * falls, and when it rises they are brought to it (exactly, save values that
+ * sink below e4m3's normal range). Rounding is to nearest even; an element that
+ * is not finite is held as NaN. Rows behind the new tokens stay as they were.
+ *
+ * A page written by a call must belong to one sequence of the call. workspace
+ * (status block, SOLATTN_WORKSPACE_BYTES) may be NULL.
+ */
+int solattn_cache_append(const void* k, const void* v, int dtype, int B, int N, const solattn_strides_t* strides,
+                         const solattn_cache_t* cache, const int32_t* table, int columns, long long table_stride,
+                         const int32_t* lengths, const int32_t* counts, void* workspace, size_t workspace_bytes,
+                         void* stream);
+
+/*
+ * Softmax attention of q [B][H][N][d] (bf16 or fp16) over the cache: H a multiple
+ * of cache->heads, head h reading key head h / (H / heads); from one query per
+ * sequence to long chunks. lengths[b] counts the sequence's tokens in the cache
+ * (the new ones among them); counts[b] (NULL: N) of the N query rows are there,
+ * and stand for the sequence's last counts[b] tokens. causal != 0: query i sees
+ * keys 0 .. lengths[b] - counts[b] + i, else all lengths[b].
+ *   out = softmax(scale q k^T) v  (q's type),  lse = ln of the sum (may be NULL)
+ * scale 0 = 1/sqrt(d). A row that sees no key gets out 0 and lse -inf; rows
+ * i >= counts[b] of out and lse stay as they were. Strides of q and out are
+ * multiples of 8 elements. workspace: solattn_cache_workspace_bytes(same sizes)
+ * bytes, its status block cleared once, used by one call at a time; nothing else
+ * in it is kept between calls. The same inputs give the same bits.
+ */
+int solattn_cache_workspace_bytes(int B, int H, int N, int d, int H_kv, int columns, size_t* bytes);
+int solattn_cache_attention(const void* q, int dtype, int B, int H, int N, int d, const solattn_strides_t* strides,
+                            const solattn_cache_t* cache, const int32_t* table, int columns, long long table_stride,
+                            const int32_t* lengths, const int32_t* counts, int causal, float scale, void* out,
+                            const solattn_strides_t* out_strides, float* lse, void* workspace, size_t workspace_bytes,
+                            void* stream);
 
 /* Static description of a status code. */
 const char* solattn_strerror(int code);
