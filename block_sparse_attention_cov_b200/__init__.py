@@ -23,8 +23,8 @@ Around attention (_rotary.py, _cache.py):
 """
 from __future__ import annotations
 
-import contextlib
 import ctypes
+import functools
 import math
 from dataclasses import dataclass
 
@@ -83,40 +83,63 @@ def _ptr(t):
     return None if t is None else ctypes.c_void_p(t.data_ptr())
 
 
+# The calls on small problems are bound by this binding, not by the GPU: the helpers below read a tensor's device as a
+# number and the stream as a handle, and share the small argument structs between calls (they are only read).
+_raw_stream = getattr(torch._C, "_cuda_getCurrentRawStream", None) or (
+    lambda index: torch.cuda.current_stream(index).cuda_stream)
+_current_index = getattr(torch._C, "_cuda_getDevice", None) or torch.cuda.current_device
+
+
+@functools.lru_cache(maxsize=512)
+def _strides_struct(batch: int, head: int, token: int):
+    return _lib.StridesStruct(batch, head, token)
+
+
 def _tensor_strides(t):
     """solattn_strides_t of one [B, H, N, d] tensor; a dimension of one element has no stride that matters."""
     if t.is_contiguous():
-        return _lib.StridesStruct(0, 0, 0)
+        return None
     B, H, N, _ = t.shape
     sb, sh, sn, _ = t.stride()
-    st = _lib.StridesStruct(sb if B > 1 else 0, sh if H > 1 else 0, sn if N > 1 else 0)
-    if B * H * N > 1 and st.batch == st.head == st.token == 0:
+    sb, sh, sn = (sb if B > 1 else 0), (sh if H > 1 else 0), (sn if N > 1 else 0)
+    if B * H * N > 1 and sb == sh == sn == 0:
         raise ValueError("a tensor of one repeated row (expand()) is not supported")
-    return st
+    return _strides_struct(sb, sh, sn)
 
 
-def _dtype(t, fp32: bool) -> int:
-    codes = {torch.bfloat16: _lib.BF16, torch.float16: _lib.F16}
-    if fp32:
-        codes[torch.float32] = _lib.F32
-    if t.dtype not in codes:
+_CODES16 = {torch.bfloat16: _lib.BF16, torch.float16: _lib.F16}
+_CODES = {**_CODES16, torch.float32: _lib.F32}
+
+
+def _dtype(t, codes=_CODES) -> int:
+    code = codes.get(t.dtype)
+    if code is None:
         raise ValueError(f"unsupported type {t.dtype}")
-    return codes[t.dtype]
+    return code
 
 
-def _same_device(*ts):
-    ts = [t for t in ts if t is not None]
-    if not all(t.is_cuda and t.device == ts[0].device for t in ts):
-        raise ValueError("all tensors must be on one CUDA device")
+def _device_index(*ts) -> int:
+    """The one CUDA device of the tensors (None: left out), as its index."""
+    dev = ts[0].get_device()
+    for t in ts:
+        if t is not None and t.get_device() != dev or dev < 0:
+            raise ValueError("all tensors must be on one CUDA device")
+    return dev
 
 
-def _current(t):
-    """The tensor's device as the current one for a call (nothing to do where it is already)."""
-    return contextlib.nullcontext() if t.device.index == torch.cuda.current_device() else torch.cuda.device(t.device)
+def _call(what: str, fn, dev: int, *args):
+    """fn(*args, stream) with the tensors' device as the current one, on that device's current stream."""
+    if dev == _current_index():
+        rc = fn(*args, _raw_stream(dev))
+    else:
+        with torch.cuda.device(dev):
+            rc = fn(*args, _raw_stream(dev))
+    if rc != _lib.OK:
+        raise SolAttnError(rc, what)
 
 
-def _stream_on(t) -> ctypes.c_void_p:
-    return ctypes.c_void_p(torch.cuda.current_stream(t.device).cuda_stream)
+def _at(t):
+    return None if t is None else t.data_ptr()
 
 
 def pooled_bytes(B: int, H: int, N: int, d: int) -> int:
@@ -136,26 +159,31 @@ class PooledStats:
     def view(self, name: str) -> torch.Tensor:
         B, H, N, d = self.shape
         nb = (N + _lib.BLOCK - 1) // _lib.BLOCK
-        dims = {
-            "qbar": (B, H, nb, d), "kbar": (B, H, nb, d), "vbar": (B, H, nb, d),
-            "kmean": (B, H, d), "kcov": (B, H, d, d), "kbar16": (B, H, nb, d), "vbar16": (B, H, nb, d),
-        }[name]
+        dims = (B, H, d) if name == "kmean" else (B, H, d, d) if name == "kcov" else (B, H, nb, d)
         dt, size = (torch.bfloat16, 2) if name.endswith("16") else (torch.float32, 4)
         off = getattr(self.struct, name) - self.buffer.data_ptr()
-        n = math.prod(dims)
-        return self.buffer[off:off + size * n].view(dt).view(dims)
+        strides = (H * d, d, 1) if name == "kmean" else (H * dims[2] * d, dims[2] * d, d, 1)
+        whole = self.buffer.view(dt)
+        return whole.as_strided(dims, strides, whole.storage_offset() + off // size)
+
+
+@functools.lru_cache(maxsize=512)
+def _pooled_offsets(B: int, H: int, N: int, d: int):
+    """(bytes, offset of every array) of solattn_pooled_layout."""
+    n, st, base = ctypes.c_size_t(0), _lib.PooledStruct(), 1 << 20
+    _check(_lib.lib().solattn_pooled_layout(B, H, N, d, base, ctypes.byref(st), ctypes.byref(n)),
+           "solattn_pooled_layout")
+    return int(n.value), tuple(getattr(st, name) - base for name, _ in _lib.PooledStruct._fields_)
 
 
 def _pooled_stats(q: torch.Tensor, stats: PooledStats | None) -> PooledStats:
     """`stats` checked against q's shape, or newly allocated ones."""
     B, H, N, d = _shape(q)
     if stats is None:
-        nbytes = pooled_bytes(B, H, N, d)
+        nbytes, offsets = _pooled_offsets(B, H, N, d)
         buf = torch.empty(nbytes, dtype=torch.uint8, device=q.device)
-        st = _lib.PooledStruct()
-        _check(_lib.lib().solattn_pooled_layout(B, H, N, d, _ptr(buf), ctypes.byref(st), None),
-               "solattn_pooled_layout")
-        stats = PooledStats(buf, st, (B, H, N, d))
+        at = buf.data_ptr()
+        stats = PooledStats(buf, _lib.PooledStruct(*[at + off for off in offsets]), (B, H, N, d))
     elif stats.shape != (B, H, N, d):
         raise ValueError("PooledStats shape does not match the inputs")
     return stats

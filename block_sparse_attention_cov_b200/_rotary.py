@@ -7,8 +7,8 @@ import math
 import torch
 
 from . import _lib
-from . import (PooledStats, _check, _check_inputs, _current, _dtype, _pooled_stats, _ptr, _same_device, _shape,
-               _stream_on, _strides, _tensor_strides)
+from . import (PooledStats, _at, _call, _check, _check_inputs, _device_index, _dtype, _pooled_stats, _strides_struct,
+               _tensor_strides)
 
 __all__ = ["Rotary", "rotary", "rotary_pool"]
 
@@ -66,74 +66,74 @@ class Rotary:
         signed = [f - (1 << 64) if f >= 1 << 63 else f for f in freq]
         self.freq = torch.tensor(signed, dtype=torch.int64).to(device)  # the 64-bit words of solattn_rotary_t.freq
         self.axis = torch.tensor(list(axis), dtype=torch.int32).to(device)
+        self._layout, self._freq, self._axis = LAYOUTS[layout], self.freq.data_ptr(), self.axis.data_ptr()
 
-    def _struct(self, positions, B: int, N: int, like: torch.Tensor):
+    def _struct(self, positions, B: int, N: int):
         """solattn_rotary_t for int32 positions [N], [B, N] (one axis) or [N, axes], [B, N, axes]."""
-        _same_device(like, self.freq, positions)
-        shape = tuple(positions.shape)
-        tail = () if self.axes == 1 else (self.axes,)
-        if positions.dtype != torch.int32 or shape not in ((N, *tail), (B, N, *tail)):
-            raise ValueError("positions must be int32 [N] or [B, N], with a last dimension of the axes when several")
-        batched = positions.dim() - len(tail) == 2
-        st = positions.stride()
-        if tail and st[-1] != 1:
-            raise ValueError("the axes of a position must be adjacent")
-        token = st[1 if batched else 0]
+        shape, st = positions.shape, positions.stride()
+        several = self.axes > 1
+        lead = len(shape) - several
+        if positions.dtype != torch.int32 or not 1 <= lead <= 2 or shape[lead - 1] != N or (lead == 2 and shape[0] != B) \
+                or (several and (shape[-1] != self.axes or st[-1] != 1)):
+            raise ValueError("positions must be int32 [N] or [B, N], with a last, contiguous dimension of the axes where "
+                             "there are several")
+        token = st[lead - 1] if N > 1 else 0
         if N > 1 and token < 1:
-            raise ValueError("positions must not repeat one token's (expand() along N)")
-        return _lib.RotaryStruct(self.rot, LAYOUTS[self.layout], self.axes, self.gain, self.freq.data_ptr(),
-                                 self.axis.data_ptr(), positions.data_ptr(), st[0] if batched and B > 1 else 0,
-                                 token if N > 1 else 0)
+            raise ValueError("positions must not be one token's repeated (expand() along N)")
+        return _lib.RotaryStruct(self.rot, self._layout, self.axes, self.gain, self._freq, self._axis, positions.data_ptr(),
+                                 st[0] if lead == 2 and B > 1 else 0, token)
 
 
-def _check_rows(x, d=None):
-    if not (x.is_cuda and x.dim() == 4 and (x.shape[-1] <= 1 or x.stride(-1) == 1)):
-        raise ValueError("expected CUDA [B, H, N, d] tensors with contiguous d")
+def _outputs(q, k, out):
+    if out is None:
+        return torch.empty_like(q), None if k is None else torch.empty_like(k)
+    for x, y in zip((q, k), out):
+        if x is not None and (y.shape != x.shape or y.dtype != x.dtype or y.stride(-1) != 1):
+            raise ValueError("out must have the inputs' shapes and type, and a contiguous d")
+    return out[0], None if k is None else out[1]
 
 
 def rotary(q, k, rope: Rotary, positions, inverse: bool = False, out=None):
     """q [B, H, N, d] and k [B, H_kv, N, d] (or None) turned by their tokens' positions, in one launch; bf16, fp16 or
     fp32, any strides with a contiguous d. Returns (q', k'). out: a pair of tensors to write (q and k themselves for in
     place). inverse turns back: the gradient of q, k from the gradient of q', k'."""
-    _check_rows(q)
-    dtype = _dtype(q, fp32=True)
-    B, H, N, d = _shape(q)
+    if q.dim() != 4 or q.stride(3) != 1 or (k is not None and (k.dim() != 4 or k.stride(3) != 1)):
+        raise ValueError("expected [B, H, N, d] tensors with contiguous d")
+    dtype = _dtype(q)
+    B, H, N, d = q.shape
+    Hk = 0
     if k is not None:
-        _check_rows(k)
-        if k.dtype != q.dtype or (k.shape[0], k.shape[2], k.shape[3]) != (B, N, d):
+        Bk, Hk, Nk, dk = k.shape
+        if k.dtype != q.dtype or (Bk, Nk, dk) != (B, N, d):
             raise ValueError("k must have q's type, batch, tokens and d")
-    q_out, k_out = out if out is not None else (torch.empty_like(q), None if k is None else torch.empty_like(k))
-    for x, y in ((q, q_out), (k, k_out)):
-        if x is None:
-            continue
-        _check_rows(y)
-        if y.shape != x.shape or y.dtype != x.dtype:
-            raise ValueError("out must have the inputs' shapes and type")
-    _same_device(q, k, q_out, k_out)
-    st = rope._struct(positions, B, N, q)
-    strides = [None if x is None else _tensor_strides(x) for x in (q, k, q_out, k_out)]
-    with _current(q):
-        _check(_lib.lib().solattn_rotary(_ptr(q), _ptr(k), _ptr(q_out), _ptr(k_out), dtype, B, H,
-                                         0 if k is None else int(k.shape[1]), N, d, *strides, st, int(inverse),
-                                         _stream_on(q)), "solattn_rotary")
+    if q.get_device() < 0:
+        raise ValueError("expected CUDA tensors")
+    q_out, k_out = _outputs(q, k, out)
+    dev = _device_index(q, k, q_out, k_out, rope.freq, positions)
+    _call("solattn_rotary", _lib.lib().solattn_rotary, dev, q.data_ptr(), _at(k), q_out.data_ptr(), _at(k_out), dtype, B, H,
+          Hk, N, d, _tensor_strides(q), None if k is None else _tensor_strides(k), _tensor_strides(q_out),
+          None if k is None else _tensor_strides(k_out), rope._struct(positions, B, N), 1 if inverse else 0)
     return q_out, k_out
 
 
 def rotary_pool(q, k, v, rope: Rotary, positions, out=None, stats: PooledStats | None = None):
-    """rotary() of bf16 q and k and pool() of the result with v, in one pass over them: returns (q', k', stats) for
-    forward(q', k', v, stats, ...). The means are those of the rotated values before their rounding. The whole head is
-    rotated (rope.rot == d). q and k share v's strides or have strides of their own layout; out as in rotary()."""
+    """rotary() of bf16 q and k [B, H, N, d] and pool() of the result with v, in one pass over the three: returns
+    (q', k', stats) for forward(q', k', v, stats, ...). The means are those of the rotated values before their rounding
+    to bf16. The whole head is rotated (rope.rot == d). q, k and v share their strides, and so do the two outputs; out
+    as in rotary()."""
     _check_inputs(q, k, v)
-    B, H, N, d = _shape(q)
-    q_out, k_out = out if out is not None else (torch.empty_like(q), torch.empty_like(k))
-    _check_inputs(q_out, k_out)
-    if q_out.shape != q.shape:
-        raise ValueError("out must have the inputs' shape")
+    B, H, N, d = q.shape
+    q_out, k_out = _outputs(q, k, out)
+    if q_out.stride() != k_out.stride():
+        raise ValueError("the outputs must share their strides")
     stats = _pooled_stats(q, stats)
-    _same_device(q, k, v, q_out, k_out, stats.buffer)
-    st = rope._struct(positions, B, N, q)
-    si, so = _strides(q), _strides(q_out)
-    with _current(q):
-        _check(_lib.lib().solattn_rotary_pool(_ptr(q), _ptr(k), _ptr(v), _ptr(q_out), _ptr(k_out), B, H, N, d, si, so, st,
-                                              ctypes.byref(stats.struct), _stream_on(q)), "solattn_rotary_pool")
+    dev = _device_index(q, k, v, q_out, k_out, stats.buffer, rope.freq, positions)
+    _call("solattn_rotary_pool", _lib.lib().solattn_rotary_pool, dev, q.data_ptr(), k.data_ptr(), v.data_ptr(),
+          q_out.data_ptr(), k_out.data_ptr(), B, H, N, d, _shared_strides(q), _shared_strides(q_out),
+          rope._struct(positions, B, N), stats.struct)
     return q_out, k_out, stats
+
+
+def _shared_strides(t):
+    """The strides as they are, for the calls that check every one of them."""
+    return None if t.is_contiguous() else _strides_struct(*t.stride()[:3])
