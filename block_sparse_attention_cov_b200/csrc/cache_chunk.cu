@@ -8,16 +8,16 @@
 // scores' accuracy) is paid once per 256 rows: 128 threads load a page's bytes,
 // convert them and store them in the swizzled operand layout.
 //
-//   warps 0-3, 4-7  softmax of tile 0 / tile 1: one thread per row, S and P in
+//   warps 0-3, 4-7  softmax of tile 0 / tile 1: one thread per row; S and P in
 //                   TMEM (P in fp16 over the first half of its own S), O scaled
 //                   in TMEM only when a row's reference moves
-//   warps 8-11      cache pages to fp16 operands: 128 keys a stage, two stages
-//   warp 12         issues every MMA: per key tile PV of the tile before, then QK,
-//                   tile 0 then tile 1, so one tile's products run while the other
-//                   tile's softmax does (warps 13-15 only give their registers)
+//   warps 8-11      cache pages to fp16 operands, four pages in shared memory
+//   warp 12         issues every MMA (warps 13-15 only give their registers)
 //
-// Bounds per key tile at d = 128 and two tiles: 2,048 cycles of tensor pipe, and
-// as many of exponentials (32,768 at 16 a cycle).
+// Keys go in tiles of two pages: one QK of 128 columns (at 64 columns the QK of a
+// tile took as long: its A operand is read from shared memory either way), then
+// softmax and PV page by page, so that PV of the first page runs under the
+// softmax of the second.
 #include <cuda_runtime.h>
 #include <cmath>
 #include <cstdint>
@@ -29,24 +29,25 @@ namespace solattn {
 namespace {
 
 constexpr int kTileRows = 128;
-constexpr int kTileKeys = 128;
 constexpr int kChunkThreads = 512;  // 16 warps, 128 registers per thread at launch
-constexpr int kStages = 2;
-constexpr int kInfo = 4;
+constexpr int kTileKeys = 2 * kPage;
+constexpr int kKStages = 2;  // key tiles
+constexpr int kVStages = 4;  // pages
+constexpr int kInfo = 8;     // pages
 
 enum : uint32_t {
   kSiteCQ = 40, kSiteCKFull, kSiteCKEmpty, kSiteCVFull, kSiteCVEmpty, kSiteCSFull, kSiteCPFull, kSiteCPv,
-  kSiteCInfo,
 };
 
 template <int D>
 struct __align__(1024) ChunkSmem {
   uint8_t q[2][kTileRows * D * 2];        // SW128 K-major panels of 128 rows
-  uint8_t k[kStages][kTileKeys * D * 2];  // the same
-  uint8_t v[kStages][kTileKeys * D * 2];  // two 64-token blocks, SW128 panels of 64 rows
-  PageScale info[kInfo][2];
-  uint64_t q_full, k_full[kStages], k_empty[kStages], v_full[kStages], v_empty[kStages];
-  uint64_t s_full[2], p_full[2], pv_done[2], info_full[kInfo], mma_done;
+  uint8_t k[kKStages][kTileKeys * D * 2]; // the same
+  uint8_t v[kVStages][kPage * D * 2];     // SW128 panels of 64 rows
+  float2 info[kInfo];                     // scales of a page's keys and values
+  uint64_t q_full[2], k_full[kKStages], k_empty[kKStages], v_full[kVStages], v_empty[kVStages];
+  uint64_t s_full[2], p_full[2][2], pv_done[2][2], mma_done;
+  float row_inv[2][kTileRows];            // factor of each query row's scores
   uint32_t tmem_base;
   int abort_flag;
   int nan;
@@ -58,27 +59,72 @@ __host__ __device__ constexpr uint32_t idesc_f16_f32(int M, int N, bool b_mn_maj
          (static_cast<uint32_t>(M >> 4) << 24);
 }
 
-// 2^k for an integral k <= 0 as an fp16 pair; 0 below fp16's range.
-__device__ __forceinline__ uint32_t pow2_f16x2(float k) {
-  const __half h = __float2half_rn(k < -30.f ? 0.f : ex2_approx(k));
-  const uint32_t u = __half_as_ushort(h);
-  return u | (u << 16);
+__device__ __forceinline__ uint64_t f2_make(uint32_t lo, uint32_t hi) {
+  uint64_t r;
+  asm("mov.b64 %0, {%1, %2};" : "=l"(r) : "r"(lo), "r"(hi));
+  return r;
 }
-__device__ __forceinline__ uint32_t mul_f16x2(uint32_t a, uint32_t b) {
-  uint32_t d;
-  asm("mul.rn.f16x2 %0, %1, %2;" : "=r"(d) : "r"(a), "r"(b));
+__device__ __forceinline__ uint64_t f2_both(float x) { return f2_make(__float_as_uint(x), __float_as_uint(x)); }
+__device__ __forceinline__ void f2_get(uint64_t v, float& lo, float& hi) {
+  asm("mov.b64 {%0, %1}, %2;" : "=f"(lo), "=f"(hi) : "l"(v));
+}
+__device__ __forceinline__ uint64_t f2_fma(uint64_t a, uint64_t b, uint64_t c) {
+  uint64_t d;
+  asm("fma.rn.f32x2 %0, %1, %2, %3;" : "=l"(d) : "l"(a), "l"(b), "l"(c));
+  return d;
+}
+__device__ __forceinline__ uint64_t f2_add(uint64_t a, uint64_t b) {
+  uint64_t d;
+  asm("add.f32x2 %0, %1, %2;" : "=l"(d) : "l"(a), "l"(b));
+  return d;
+}
+__device__ __forceinline__ float max3(float a, float b, float c) {
+  float d;
+  asm("max.f32 %0, %1, %2, %3;" : "=f"(d) : "f"(a), "f"(b), "f"(c));
   return d;
 }
 
-// Rare paths, out of line; warp-collective, a lane with factor 1 keeps its row.
-static __device__ __noinline__ void scale_p_half(uint32_t taddr, float k) {
-  const uint32_t f = pow2_f16x2(k);
-  uint32_t pw[32];
-  tmem_ld32_wait(taddr, pw);
+// The largest of a row's 64 scores of a page.
+__device__ __forceinline__ float page_max(const uint32_t (&sv)[64]) {
+  float t[4] = {-INFINITY, -INFINITY, -INFINITY, -INFINITY};
 #pragma unroll
-  for (int i = 0; i < 32; ++i) pw[i] = mul_f16x2(pw[i], f);
-  tmem_st32_wait(taddr, pw);
+  for (int i = 0; i < 64; i += 8)
+#pragma unroll
+    for (int e = 0; e < 4; ++e)
+      t[e] = max3(t[e], __uint_as_float(sv[i + 2 * e]), __uint_as_float(sv[i + 2 * e + 1]));
+  return fmaxf(max3(t[0], t[1], t[2]), t[3]);
 }
+// P = 2^(s c + add) of the page as 32 fp16 pairs; returns the sum.
+__device__ __forceinline__ float page_weights(const uint32_t (&sv)[64], float c, float add, uint32_t* pw) {
+  const uint64_t c2 = f2_both(c), a2 = f2_both(add);
+  uint64_t l0 = 0, l1 = 0;
+#pragma unroll
+  for (int i = 0; i < 32; i += 2) {
+    float x0, x1, y0, y1;
+    f2_get(f2_fma(f2_make(sv[2 * i], sv[2 * i + 1]), c2, a2), x0, x1);
+    f2_get(f2_fma(f2_make(sv[2 * i + 2], sv[2 * i + 3]), c2, a2), y0, y1);
+    x0 = ex2_approx(x0);
+    x1 = ex2_approx(x1);
+    y0 = ex2_approx(y0);
+    y1 = ex2_approx(y1);
+    l0 = f2_add(l0, f2_make(__float_as_uint(x0), __float_as_uint(x1)));
+    l1 = f2_add(l1, f2_make(__float_as_uint(y0), __float_as_uint(y1)));
+    pw[i] = pack_f16x2(x0, x1);
+    pw[i + 1] = pack_f16x2(y0, y1);
+  }
+  float u, v;
+  f2_get(f2_add(l0, l1), u, v);
+  return u + v;
+}
+// Log2 units per unit of a row's dot products; never 0, which would turn a
+// masked key's -inf into NaN.
+__device__ __forceinline__ float row_scale(const PageScale& ps, float rf) { return fmaxf(ps.ck * rf, 1.17549435e-38f); }
+// The exponent's addend of a page for a row with reference m.
+__device__ __forceinline__ float page_addend(const PageScale& ps, float m) {
+  return ps.vinv == 0.f ? -INFINITY : ps.ev + kPBias - (m == -INFINITY ? 0.f : m);
+}
+
+// Rare paths, out of line; warp-collective, a lane with factor 1 keeps its row.
 template <int D>
 static __device__ __noinline__ void scale_o(uint32_t taddr, float f) {
 #pragma unroll 1
@@ -105,6 +151,77 @@ __device__ __forceinline__ void st_shared_v4(void* p, uint32_t a, uint32_t b, ui
   asm volatile("st.shared.v4.b32 [%0], {%1,%2,%3,%4};" ::"r"(smem_u32(p)), "r"(a), "r"(b), "r"(c), "r"(d) : "memory");
 }
 
+// 32 rows of queries into the operand layout, scaled to fp16's range by a power
+// of two per row: copied as they are (a row's lanes side by side, so that a copy
+// touches a few lines and not one per lane), then converted in place.
+template <typename Elem, int D>
+__device__ __forceinline__ void load_queries(const CacheAttnArgs& a, uint8_t* tile, float* row_inv, int b, int hk,
+                                             int first, int rows, int wq, int lane) {
+  constexpr int LPR = D / 8, RPL = 32 / LPR;  // lanes per row, rows per step
+  const int ch = lane % LPR;
+  uint8_t* at = tile + (ch / 8) * (kTileRows * 128);
+#pragma unroll 2
+  for (int i = 0; i < 32 / RPL; ++i) {
+    const int lr = wq * 32 + i * RPL + lane / LPR, r = first + lr;
+    int qi, g;
+    row_place(a, r, &qi, &g);
+    const uint16_t* src = a.q + b * a.st.b + (hk * a.group + g) * a.st.h + static_cast<long long>(qi) * a.st.n + 8 * ch;
+    asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(smem_u32(at + sw128(lr, ch % 8))),
+                 "l"(r < rows ? src : a.q), "r"(r < rows ? 16 : 0)
+                 : "memory");
+  }
+  asm volatile("cp.async.wait_all;" ::: "memory");
+#pragma unroll 4
+  for (int i = 0; i < 32 / RPL; ++i) {  // every lane reads back what it copied
+    const int lr = wq * 32 + i * RPL + lane / LPR;
+    uint4* p = reinterpret_cast<uint4*>(at + sw128(lr, ch % 8));
+    const uint4 w = *p;
+    const uint32_t u[4] = {w.x, w.y, w.z, w.w};
+    float2 f[4];
+    float amax = 0.f;
+#pragma unroll
+    for (int e = 0; e < 4; ++e) {
+      f[e] = unpack2<Elem>(u[e]);
+      amax = fmaxf(amax, fmaxf(fabsf(f[e].x), fabsf(f[e].y)));
+    }
+#pragma unroll
+    for (int off = LPR / 2; off > 0; off >>= 1) amax = fmaxf(amax, __shfl_xor_sync(0xffffffffu, amax, off));
+    float mul, inv;
+    row_factor(amax, &mul, &inv);
+    *p = make_uint4(pack_f16x2(f[0].x * mul, f[0].y * mul), pack_f16x2(f[1].x * mul, f[1].y * mul),
+                    pack_f16x2(f[2].x * mul, f[2].y * mul), pack_f16x2(f[3].x * mul, f[3].y * mul));
+    if (ch == 0) row_inv[lr] = inv;
+  }
+  fence_proxy_async_smem();
+  __syncwarp();
+}
+
+// A warp's 32 rows of D / 2 columns (half 0 or 1 of the row; columns of 4 bytes
+// for parts, 2 for results) from its stage in shared memory to their rows in
+// memory: a row's lanes side by side. Row r's 16-byte pieces are rotated by r.
+template <int PIECES>
+__device__ __forceinline__ void store_rows(const CacheAttnArgs& a, const uint8_t* stage, int b, int hk, int first,
+                                           int rows, int half, int split, int lane) {
+  constexpr int RPL = 32 / PIECES;
+  const int e = lane % PIECES;
+#pragma unroll 4
+  for (int i = 0; i < 32 / RPL; ++i) {
+    const int row = i * RPL + lane / PIECES, r = first + row;
+    if (r < rows) {
+      const uint4 v = *reinterpret_cast<const uint4*>(stage + (row * PIECES + ((e + row) % PIECES)) * 16);
+      int qi, g;
+      row_place(a, r, &qi, &g);
+      const int h = hk * a.group + g;
+      if (a.splits > 1)
+        *reinterpret_cast<uint4*>(a.part_o + partial_row(a, b, h, qi, split) * a.d + half * (a.d / 2) + 4 * e) = v;
+      else
+        *reinterpret_cast<uint4*>(a.out + b * a.ost.b + h * a.ost.h + static_cast<long long>(qi) * a.ost.n +
+                                  half * (a.d / 2) + 8 * e) = v;
+    }
+  }
+  __syncwarp();
+}
+
 template <typename Elem, int D>
 __global__ void __launch_bounds__(kChunkThreads, 1) cache_chunk_kernel(const CacheAttnArgs a, int tiles) {
   extern __shared__ uint8_t smem_raw[];
@@ -116,6 +233,29 @@ __global__ void __launch_bounds__(kChunkThreads, 1) cache_chunk_kernel(const Cac
   const int hk = blockIdx.y, b = blockIdx.z;
   DeviceStatus* st = a.status;
   volatile int* abort_flag = &sm.abort_flag;
+  if (tid == 0) {
+    for (int i = 0; i < kKStages; ++i) {
+      mbar_init(&sm.k_full[i], 8);  // four warps, two pages
+      mbar_init(&sm.k_empty[i], 1);
+    }
+    for (int i = 0; i < kVStages; ++i) {
+      mbar_init(&sm.v_full[i], 4);
+      mbar_init(&sm.v_empty[i], 1);
+    }
+    for (int i = 0; i < 2; ++i) {
+      mbar_init(&sm.s_full[i], 2);  // the MMAs' commit, and the issuer itself, which passes on the page scales
+      for (int e = 0; e < 2; ++e) {
+        mbar_init(&sm.p_full[i][e], 4);
+        mbar_init(&sm.pv_done[i][e], 1);
+      }
+    }
+    for (int i = 0; i < 2; ++i) mbar_init(&sm.q_full[i], 4);
+    mbar_init(&sm.mma_done, 1);
+    sm.abort_flag = 0;
+    sm.nan = 0;
+    fence_barrier_init();
+  }
+  __syncthreads();
   const Extent ex = extent(a, b, split == 0 && hk == 0 && mt == 0 && tid == 0);
   const int rows = ex.cnt * a.group;
   const int r0 = mt * 2 * kTileRows;
@@ -124,86 +264,78 @@ __global__ void __launch_bounds__(kChunkThreads, 1) cache_chunk_kernel(const Cac
   const int last_row = min(rows, r0 + 2 * kTileRows) - 1;
   const int seen = key_limit(ex, a.causal, last_row / a.group);  // keys that some row sees
   const int least = key_limit(ex, a.causal, r0 / a.group);       // keys that every row sees
-  const int ktiles = (seen + kTileKeys - 1) / kTileKeys;
-  const int per = (ktiles + a.splits - 1) / a.splits;
-  const int t0 = min(ktiles, split * per), T = min(ktiles, t0 + per) - t0;
+  const int pages = (seen + kPage - 1) / kPage;
+  const int per = (pages + a.splits - 1) / a.splits;
+  const int c0 = min(pages, split * per);
+  const int P = (min(pages, c0 + per) - c0 + 1) / 2 * 2;  // this part's pages, rounded up to whole key tiles
+  const int pend = min(pages, c0 + per) - c0;             // those that are there
 
-  if (tid == 0) {
-    mbar_init(&sm.q_full, 4 * nq);
-    for (int i = 0; i < kStages; ++i) {
-      mbar_init(&sm.k_full[i], 4);
-      mbar_init(&sm.v_full[i], 4);
-      mbar_init(&sm.k_empty[i], 1);
-      mbar_init(&sm.v_empty[i], 1);
-    }
-    for (int i = 0; i < 2; ++i) {
-      mbar_init(&sm.s_full[i], 1);
-      mbar_init(&sm.p_full[i], 4);
-      mbar_init(&sm.pv_done[i], 1);
-    }
-    for (int i = 0; i < kInfo; ++i) mbar_init(&sm.info_full[i], 1);
-    mbar_init(&sm.mma_done, 1);
-    sm.abort_flag = 0;
-    sm.nan = 0;
-    fence_barrier_init();
-  }
-  if (warp == 12) {
-    tmem_alloc(&sm.tmem_base, 512);
-    tmem_relinquish();
-  }
-  tc_fence_before();
-  __syncthreads();
-  tc_fence_after();
-  const uint32_t tmem = sm.tmem_base;
-  // TMEM columns: S / P of tile 0 at 0, of tile 1 at 128; O of tile 0 at 256, of tile 1 at 384
+  // TMEM columns: S of tile x at 128 x, P of its page e over the first half of that page's scores (128 x + 64 e);
+  // O of tile x at 256 + 128 x
 
   // Registers: 152 for the 256 softmax threads, 104 for the other 256 (65,536 in all).
   if (warp >= 12) {
     regs_dec<104>();
     if (warp == 12) {
     // ======================= MMA issuer =======================
+    tmem_alloc(&sm.tmem_base, 512);  // the softmax warps learn of it with the first scores
+    tmem_relinquish();
+    __syncwarp();
+    const uint32_t tmem = *static_cast<volatile uint32_t*>(&sm.tmem_base);
     constexpr uint32_t idesc_qk = idesc_f16_f32(kTileRows, kTileKeys, false);
     constexpr uint32_t idesc_pv = idesc_f16_f32(kTileRows, D, true);
     const uint64_t qd0 = sw128_desc(smem_u32(&sm.q[0][0]), 16, 1024);
     const uint64_t kd0 = sw128_desc(smem_u32(&sm.k[0][0]), 16, 1024);
     const uint64_t vd0 = sw128_desc(smem_u32(&sm.v[0][0]), 8192, 1024);
-    bool ok = T == 0 || chunk_wait(&sm.q_full, 0, abort_flag, st, kSiteCQ, blockIdx.x);
-    for (int t = 0; t <= T && T > 0 && ok; ++t) {
-      if (t < T) ok = chunk_wait(&sm.k_full[t % kStages], (t / kStages) & 1, abort_flag, st, kSiteCKFull, blockIdx.x);
-      if (t > 0 && ok)
-        ok = chunk_wait(&sm.v_full[(t - 1) % kStages], ((t - 1) / kStages) & 1, abort_flag, st, kSiteCVFull,
-                        blockIdx.x);
+    // QK of key tile t for tile x
+    auto qk = [&](int t, int x) {
+      tc_fence_after();
+      if (elect_one()) {
+        const uint64_t kd = kd0 + ((t % kKStages) * (kTileKeys * D * 2) >> 4);
+        const uint64_t qd = qd0 + (x * (kTileRows * D * 2) >> 4);
+#pragma unroll
+        for (int kk = 0; kk < D / 16; ++kk) {
+          const uint32_t off = ((kk / 4) * (kTileRows * 128) + (kk % 4) * 32) >> 4;
+          mma_ss(tmem + x * 128, qd + off, kd + off, idesc_qk, kk > 0 ? 1u : 0u);
+        }
+        mbar_arrive(&sm.s_full[x]);
+        mma_commit(&sm.s_full[x]);
+        if (x == nq - 1) mma_commit(&sm.k_empty[t % kKStages]);
+      }
+      __syncwarp();
+    };
+    auto k_there = [&](int t) {
+      return chunk_wait(&sm.k_full[t % kKStages], (t / kKStages) & 1, abort_flag, st, kSiteCKFull, blockIdx.x);
+    };
+    const int T = P / 2;
+    bool ok = T == 0 || k_there(0);
+    for (int x = 0; x < nq && ok && T > 0; ++x) {
+      ok = chunk_wait(&sm.q_full[x], 0, abort_flag, st, kSiteCQ, blockIdx.x);
+      if (ok) qk(0, x);
+    }
+    for (int t = 0; t < T && ok; ++t) {
+      if (t + 1 < T) ok = k_there(t + 1);
       for (int x = 0; x < nq && ok; ++x) {
-        if (t > 0) {  // PV of the tile before
-          ok = chunk_wait(&sm.p_full[x], (t - 1) & 1, abort_flag, st, kSiteCPFull, blockIdx.x);
+        for (int e = 0; e < 2 && ok; ++e) {
+          const int p = 2 * t + e;
+          if (x == 0) ok = chunk_wait(&sm.v_full[p % kVStages], (p / kVStages) & 1, abort_flag, st, kSiteCVFull, blockIdx.x);
+          if (ok) ok = chunk_wait(&sm.p_full[x][e], t & 1, abort_flag, st, kSiteCPFull, blockIdx.x);
           if (!ok) break;
           tc_fence_after();
           if (elect_one()) {
-            const uint32_t vst = (t - 1) % kStages;
-            for (int kk = 0; kk < kTileKeys / 16; ++kk) {
-              const uint32_t off = vst * (kTileKeys * D * 2) + (kk / 4) * (kPage * D * 2) + (kk % 4) * 2048;
-              mma_ts(tmem + 256 + x * 128, tmem + x * 128 + kk * 8, vd0 + (off >> 4), idesc_pv,
-                     (t > 1 || kk > 0) ? 1u : 0u);
-            }
-            mma_commit(&sm.pv_done[x]);
-            if (x == nq - 1) mma_commit(&sm.v_empty[vst]);
+            const uint64_t vd = vd0 + ((p % kVStages) * (kPage * D * 2) >> 4);
+#pragma unroll
+            for (int kk = 0; kk < kPage / 16; ++kk)
+              mma_ts(tmem + 256 + x * 128, tmem + x * 128 + e * 64 + kk * 8, vd + ((kk * 2048) >> 4), idesc_pv,
+                     (p > 0 || kk > 0) ? 1u : 0u);
+            mma_commit(&sm.pv_done[x][e]);
+            if (x == nq - 1) mma_commit(&sm.v_empty[p % kVStages]);
           }
           __syncwarp();
         }
-        if (t < T) {  // QK: after the PV that reads P from the same columns (issued by this thread, in order)
-          tc_fence_after();
-          if (elect_one()) {
-            const uint32_t kst = t % kStages;
-            for (int kk = 0; kk < D / 16; ++kk) {
-              const uint32_t off = (kk / 4) * (kTileRows * 128) + (kk % 4) * 32;
-              mma_ss(tmem + x * 128, qd0 + ((x * (kTileRows * D * 2) + off) >> 4),
-                     kd0 + ((kst * (kTileKeys * D * 2) + off) >> 4), idesc_qk, kk > 0 ? 1u : 0u);
-            }
-            mma_commit(&sm.s_full[x]);
-            if (x == nq - 1) mma_commit(&sm.k_empty[kst]);
-          }
-          __syncwarp();
-        }
+        // the next key tile's scores, behind the PV that reads P from the same
+        // columns (one thread's MMAs execute in order)
+        if (ok && t + 1 < T) qk(t + 1, x);
       }
     }
     if (elect_one()) mma_commit(&sm.mma_done);  // teardown: issued MMAs complete before TMEM is freed
@@ -215,106 +347,104 @@ __global__ void __launch_bounds__(kChunkThreads, 1) cache_chunk_kernel(const Cac
     regs_dec<104>();
     // ======================= cache pages to fp16 operands =======================
     const int ct = tid - 256;
-    constexpr int LPR = D / 16;               // lanes per row (16 bytes each)
-    constexpr int ROWS = 128 / LPR;           // rows per pass of the 128 threads
-    constexpr int PASSES = kTileKeys / ROWS;  // 8 (d = 128) or 4
-    const int c = ct % LPR, rr = ct / LPR;
-    const long long lane_off = static_cast<long long>(hk) * kPage * D + 16 * c;
-    const int32_t* table = a.table + b * a.table_stride;
-    const int npages = (ex.len + kPage - 1) / kPage;
-    // pages of key tile t (-1: not there)
-    auto pages_of = [&](int t, int (&pg)[2]) {
-#pragma unroll
-      for (int x = 0; x < 2; ++x) {
-        const int col = (t0 + t) * 2 + x;
-        pg[x] = -1;
-        if (t < T && col < npages) {
-          pg[x] = __ldg(table + col);
-          if (pg[x] < 0 || pg[x] >= a.pages) {
-            report_page(st, b);
-            pg[x] = -1;
-          }
-        }
-      }
+    constexpr int LPR = D / 16;           // lanes per row (16 bytes each)
+    constexpr int ROWS = 128 / LPR;       // rows per pass of the 128 threads
+    constexpr int PASSES = kPage / ROWS;  // 4 (d = 128) or 2
+    // chunk of the row and row of the pass: eight neighbouring lanes take four chunks of two rows
+    const int c = LPR == 4 ? ct % 4 : ct % 4 + 4 * (ct / 8 % 2);
+    const int rr = LPR == 4 ? ct / 4 : ct / 4 % 2 + 2 * (ct / 16);
+    const long long lane_off = static_cast<long long>(hk) * kPage * D + rr * D + 16 * c;
+    const int32_t* table = a.table + b * a.table_stride + c0;
+    // the table's entry for step p (-1: no such step), and what is made of it when it is used
+    auto entry = [&](int p) { return p < pend ? __ldg(table + p) : -1; };
+    auto checked = [&](int pg, int p) {
+      if (pg >= 0 && pg < a.pages) return pg;
+      if (p < pend) report_page(st, b);
+      return -1;
     };
-    auto load = [&](uint4 (&w)[PASSES], const uint8_t* src, const int (&pg)[2], int row_end) {
+    auto load = [&](uint4 (&w)[PASSES], const uint8_t* src, int pg, int row_end) {
 #pragma unroll
-      for (int i = 0; i < PASSES; ++i) {
-        const int row = i * ROWS + rr;
-        const int p = row < kPage ? pg[0] : pg[1];
-        w[i] = (p >= 0 && row < row_end)
-                   ? __ldg(reinterpret_cast<const uint4*>(src + p * a.page_stride + lane_off + (row % kPage) * D))
+      for (int i = 0; i < PASSES; ++i)
+        w[i] = (pg >= 0 && i * ROWS + rr < row_end)
+                   ? __ldg(reinterpret_cast<const uint4*>(src + pg * a.page_stride + lane_off + i * ROWS * D))
                    : make_uint4(0, 0, 0, 0);
-      }
     };
-    // 16 e4m3 of a row: two 16-byte chunks of fp16; lanes of the second panel
-    // store theirs in the other order, so that a quarter-warp's eight stores
-    // (one row, or two) fall into different banks
-    auto store = [&](const uint4 (&w)[PASSES], uint8_t* dst, int panel_rows, int block_rows) {
+    // 16 e4m3 of a row become two 16-byte chunks of fp16. A quarter-warp's eight
+    // stores cover two rows' chunks of one panel: eight different bank groups.
+    const int ch = 2 * (c % 4);
+    const uint32_t off0 = sw128(rr, ch), off1 = sw128(rr, ch + 1);  // ROWS is a multiple of the swizzle's 8 rows
+    auto store = [&](const uint4 (&w)[PASSES], uint8_t* dst, int panel_rows) {
+      uint8_t* base = dst + (c / 4) * (panel_rows * 128);
 #pragma unroll
       for (int i = 0; i < PASSES; ++i) {
-        const int row = i * ROWS + rr;
-        uint8_t* base = dst + (row / block_rows) * (block_rows * D * 2) + (c / 4) * (panel_rows * 128);
-        const int r = row % block_rows;
-        const uint32_t u[4] = {w[i].x, w[i].y, w[i].z, w[i].w};
         uint32_t f[8];
-#pragma unroll
-        for (int e = 0; e < 4; ++e) {
-          f[2 * e] = e4m3x2_f16x2(u[e] & 0xffffu);
-          f[2 * e + 1] = e4m3x2_f16x2(u[e] >> 16);
-        }
-        const int ch = 2 * (c % 4);
-        if (c < 4) {
-          st_shared_v4(base + sw128(r, ch), f[0], f[1], f[2], f[3]);
-          st_shared_v4(base + sw128(r, ch + 1), f[4], f[5], f[6], f[7]);
-        } else {
-          st_shared_v4(base + sw128(r, ch + 1), f[4], f[5], f[6], f[7]);
-          st_shared_v4(base + sw128(r, ch), f[0], f[1], f[2], f[3]);
-        }
+        e4m3x4_f16(w[i].x, f[0], f[1]);
+        e4m3x4_f16(w[i].y, f[2], f[3]);
+        e4m3x4_f16(w[i].z, f[4], f[5]);
+        e4m3x4_f16(w[i].w, f[6], f[7]);
+        st_shared_v4(base + off0 + i * ROWS * 128, f[0], f[1], f[2], f[3]);
+        st_shared_v4(base + off1 + i * ROWS * 128, f[4], f[5], f[6], f[7]);
       }
     };
-    uint4 kw[PASSES], vw[PASSES];
-    int pg[2], pn[2];
-    pages_of(0, pg);
-    if (T > 0) load(kw, a.k, pg, kTileKeys);
-    for (int t = 0; t < T; ++t) {
-      const int s = t % kStages;
-      const uint32_t ph = ((t / kStages) & 1) ^ 1;
-      const int key0 = (t0 + t) * kTileKeys;
-      load(vw, a.v, pg, ex.len - key0);  // rows behind the sequence as zeros: they may hold NaN
-      pages_of(t + 1, pn);
-      float ks = 0.f, vs = 0.f;
-      if (ct < 2 && pg[ct] >= 0) {
-        ks = __ldg(a.k_scale + pg[ct] * a.scale_stride + hk);
-        vs = __ldg(a.v_scale + pg[ct] * a.scale_stride + hk);
+    // Two pages of loads in flight in registers (a page takes about the time of
+    // one round trip to memory), their numbers a further two pages ahead.
+    uint4 kw[2][PASSES], vw[2][PASSES];
+    float ks[2], vs[2];
+    int next[2];
+    auto fetch_scale = [&](int e, int pg) {
+      ks[e] = vs[e] = 0.f;
+      if (ct == 0 && pg >= 0) {
+        ks[e] = __ldg(a.k_scale + pg * a.scale_stride + hk);
+        vs[e] = __ldg(a.v_scale + pg * a.scale_stride + hk);
       }
-      if (t >= kStages && !chunk_wait(&sm.k_empty[s], ph, abort_flag, st, kSiteCKEmpty, blockIdx.x)) break;
-      if (ct < 2) sm.info[t % kInfo][ct] = page_scale(a, ks, vs);
-      store(kw, sm.k[s], kTileKeys, kTileKeys);
-      fence_proxy_async_smem();
-      __syncwarp();
-      if (lane == 0) {
-        // the page scales were written by lanes 0 and 1 of the first of these warps
-        if (warp == 8) mbar_arrive(&sm.info_full[t % kInfo]);
-        mbar_arrive(&sm.k_full[s]);
-      }
-      if (t + 1 < T) load(kw, a.k, pn, kTileKeys);
-      if (a.causal && key0 + kTileKeys > least) {  // a NaN value must reach only the rows that see its token
-        bool bad = false;
+    };
+    auto fetch_v = [&](int e, int pg, int p) {  // rows behind the sequence as zeros: they may hold NaN
+      load(vw[e], a.v, pg, ex.len - (c0 + p) * kPage);
+    };
 #pragma unroll
-        for (int i = 0; i < PASSES; ++i) {
-          bad |= has_nan8(vw[i].x) | has_nan8(vw[i].y) | has_nan8(vw[i].z) | has_nan8(vw[i].w);
-          vw[i] = make_uint4(drop_nan8(vw[i].x), drop_nan8(vw[i].y), drop_nan8(vw[i].z), drop_nan8(vw[i].w));
+    for (int e = 0; e < 2; ++e) {
+      const int pg = checked(entry(e), e);
+      next[e] = entry(2 + e);
+      load(kw[e], a.k, pg, kPage);
+      fetch_v(e, pg, e);
+      fetch_scale(e, pg);
+    }
+    bool ok = true;
+    for (int t = 0; t < P / 2 && ok; ++t) {
+      const int kst = t % kKStages;
+      if (t >= kKStages)
+        ok = chunk_wait(&sm.k_empty[kst], ((t / kKStages) & 1) ^ 1, abort_flag, st, kSiteCKEmpty, blockIdx.x);
+#pragma unroll
+      for (int e = 0; e < 2; ++e) {
+        const int p = 2 * t + e, vst = p % kVStages;
+        const int pg = checked(next[e], p + 2);
+        next[e] = entry(p + 4);
+        // the scales' slot held page p - 8, past in both tiles: the QK of pages p - 4 was issued behind P(p - 5)
+        if (ct == 0) sm.info[p % kInfo] = make_float2(ks[e], vs[e]);
+        store(kw[e], sm.k[kst] + e * kPage * 128, kTileKeys);
+        fence_proxy_async_smem();
+        __syncwarp();
+        if (lane == 0) mbar_arrive(&sm.k_full[kst]);
+        load(kw[e], a.k, pg, kPage);
+        fetch_scale(e, pg);
+        if (a.causal && (c0 + p + 1) * kPage > least) {  // a NaN value must reach only the rows that see its token
+          bool bad = false;
+#pragma unroll
+          for (int i = 0; i < PASSES; ++i) {
+            uint4& w = vw[e][i];
+            bad |= has_nan8(w.x) | has_nan8(w.y) | has_nan8(w.z) | has_nan8(w.w);
+            w = make_uint4(drop_nan8(w.x), drop_nan8(w.y), drop_nan8(w.z), drop_nan8(w.w));
+          }
+          if (bad) sm.nan = 1;
         }
-        if (bad) sm.nan = 1;
+        if (ok && p >= kVStages)
+          ok = chunk_wait(&sm.v_empty[vst], ((p / kVStages) & 1) ^ 1, abort_flag, st, kSiteCVEmpty, blockIdx.x);
+        store(vw[e], sm.v[vst], kPage);
+        fence_proxy_async_smem();
+        __syncwarp();
+        if (lane == 0) mbar_arrive(&sm.v_full[vst]);
+        fetch_v(e, pg, p + 2);
       }
-      if (t >= kStages && !chunk_wait(&sm.v_empty[s], ph, abort_flag, st, kSiteCVEmpty, blockIdx.x)) break;
-      store(vw, sm.v[s], kPage, kPage);
-      fence_proxy_async_smem();
-      __syncwarp();
-      if (lane == 0) mbar_arrive(&sm.v_full[s]);
-      pg[0] = pn[0];
-      pg[1] = pn[1];
     }
   } else {
     regs_inc<152>();
@@ -324,141 +454,110 @@ __global__ void __launch_bounds__(kChunkThreads, 1) cache_chunk_kernel(const Cac
     const int lr = wq * 32 + lane;  // row of the tile == TMEM lane
     const int r = r0 + x * kTileRows + lr;
     const bool there = r < rows;
-    const int qi = r / a.group, h = hk * a.group + r % a.group;
-    const int lim = there ? key_limit(ex, a.causal, qi) : 0;
+    int qi, g;
+    row_place(a, r, &qi, &g);
+    const int h = hk * a.group + g;
+    const int lim = there ? key_limit(ex, a.causal, qi) : seen;  // a row that is not there masks nothing by itself
     const uint32_t lane_sel = static_cast<uint32_t>(wq * 32) << 16;
-    const uint32_t colS = tmem + x * 128 + lane_sel, colO = tmem + 256 + x * 128 + lane_sel;
-    // ---- the row of Q, scaled to fp16's range, into the operand layout
-    float rf;
-    {
-      const uint16_t* src = a.q + b * a.st.b + h * a.st.h + static_cast<long long>(qi) * a.st.n;
-      uint4 w[D / 8];
-      float amax = 0.f;
-#pragma unroll
-      for (int i = 0; i < D / 8; ++i) {
-        w[i] = there ? __ldg(reinterpret_cast<const uint4*>(src + 8 * i)) : make_uint4(0, 0, 0, 0);
-        const uint32_t u[4] = {w[i].x, w[i].y, w[i].z, w[i].w};
-#pragma unroll
-        for (int e = 0; e < 4; ++e) {
-          const float2 f = unpack2<Elem>(u[e]);
-          amax = fmaxf(amax, fmaxf(fabsf(f.x), fabsf(f.y)));
-        }
-      }
-      float mul;
-      row_factor(amax, &mul, &rf);
-#pragma unroll
-      for (int i = 0; i < D / 8; ++i) {
-        const uint32_t u[4] = {w[i].x, w[i].y, w[i].z, w[i].w};
-        uint32_t p[4];
-#pragma unroll
-        for (int e = 0; e < 4; ++e) {
-          const float2 f = unpack2<Elem>(u[e]);
-          p[e] = pack_f16x2(f.x * mul, f.y * mul);
-        }
-        st_shared_v4(&sm.q[x][(i / 8) * (kTileRows * 128) + sw128(lr, i % 8)], p[0], p[1], p[2], p[3]);
-      }
-      fence_proxy_async_smem();
-      __syncwarp();
-      if (lane == 0) mbar_arrive(&sm.q_full);
-    }
+    load_queries<Elem, D>(a, sm.q[x], sm.row_inv[x], b, hk, r0 + x * kTileRows, rows, wq, lane);
+    if (lane == 0) mbar_arrive(&sm.q_full[x]);
+    const float rf = sm.row_inv[x][lr];
+    uint32_t colS = 0, colO = 0;
     float m = -INFINITY, l = 0.f;
     bool ok = true;
-    for (int t = 0; t < T; ++t) {
-      ok = chunk_wait<1>(&sm.info_full[t % kInfo], (t / kInfo) & 1, abort_flag, st, kSiteCInfo, blockIdx.x);
-      if (ok) ok = chunk_wait<1>(&sm.s_full[x], t & 1, abort_flag, st, kSiteCSFull, blockIdx.x);
-      if (!ok) break;
-      tc_fence_after();
-      const int key0 = (t0 + t) * kTileKeys;
-      float mn = m, lt = 0.f;
-#pragma unroll 1
-      for (int hh = 0; hh < 2; ++hh) {  // one page at a time
-        const PageScale ps = sm.info[t % kInfo][hh];
-        uint32_t sv[64];
-        tmem_ld32x2_wait(colS + hh * 64, colS + hh * 64 + 32, sv);
-        const int valid = lim - (key0 + hh * kPage);
-        if (__any_sync(0xffffffffu, valid < kPage)) {
-#pragma unroll
-          for (int i = 0; i < 64; ++i)
-            if (i >= valid) sv[i] = 0xff800000u;
-        }
-        float mx = -INFINITY;
-#pragma unroll
-        for (int i = 0; i < 64; i += 2) mx = fmaxf(mx, fmaxf(__uint_as_float(sv[i]), __uint_as_float(sv[i + 1])));
-        // never 0, which would turn a masked key's -inf into NaN
-        const float c = fmaxf(ps.ck * rf, 1.17549435e-38f);
-        const float tm = mx == -INFINITY || ps.vinv == 0.f ? -INFINITY : fmaf(mx, c, ps.ev);
-        if (__any_sync(0xffffffffu, tm > mn + kSlack)) {
-          const float up = tm > mn + kSlack ? ceilf(tm) : mn;
-          if (hh == 1) {  // the first page's P and sum follow
-            scale_p_half(colS, mn == up || mn == -INFINITY ? 0.f : mn - up);
-            lt = mn == up ? lt : (mn == -INFINITY ? lt : lt * ex2_approx(mn - up));
-          }
-          mn = up;
-        }
-        const float add = ps.vinv == 0.f ? -INFINITY : ps.ev + kPBias - (mn == -INFINITY ? 0.f : mn);
-        float s0 = 0.f, s1 = 0.f;
-        uint32_t pw[32];
-#pragma unroll
-        for (int i = 0; i < 32; ++i) {
-          const float p0 = ex2_approx(fmaf(__uint_as_float(sv[2 * i]), c, add));
-          const float p1 = ex2_approx(fmaf(__uint_as_float(sv[2 * i + 1]), c, add));
-          s0 += p0;
-          s1 += p1;
-          pw[i] = pack_f16x2(p0, p1);
-        }
-        lt = fmaf(s0 + s1, ps.vinv, lt);
-        tmem_st32_wait(colS + hh * 32, pw);
-      }
-      // ---- O and the sum follow the reference (rare after the first tiles)
-      const bool moved = mn != m && m != -INFINITY;
-      if (__any_sync(0xffffffffu, moved)) {
-        // here t > 0: the PV of the tile before has to be complete
-        ok = chunk_wait<1>(&sm.pv_done[x], (t - 1) & 1, abort_flag, st, kSiteCPv, blockIdx.x);
+    const int lim_warp = __reduce_min_sync(0xffffffffu, lim);
+    for (int p = 0; p < P; ++p) {
+      if ((p & 1) == 0) {
+        ok = chunk_wait<1>(&sm.s_full[x], (p >> 1) & 1, abort_flag, st, kSiteCSFull, blockIdx.x);
         if (!ok) break;
         tc_fence_after();
-        scale_o<D>(colO, moved ? ex2_approx(m - mn) : 1.f);
+        if (p == 0) {
+          const uint32_t tmem = *static_cast<volatile uint32_t*>(&sm.tmem_base);
+          colS = tmem + x * 128 + lane_sel;
+          colO = tmem + 256 + x * 128 + lane_sel;
+        }
       }
-      l = fmaf(l, m == mn || m == -INFINITY ? 1.f : ex2_approx(m - mn), lt);
-      m = mn;
+      const float2 kv = sm.info[p % kInfo];
+      const PageScale ps = page_scale(a, kv.x, kv.y);
+      const uint32_t col = colS + (p & 1) * 64;
+      uint32_t sv[64], pw[32];
+      tmem_ld32x2_wait(col, col + 32, sv);
+      const int key0 = (c0 + p) * kPage;
+      if (key0 + kPage > lim_warp) {
+#pragma unroll
+        for (int i = 0; i < 64; ++i)
+          if (key0 + i >= lim) sv[i] = 0xff800000u;
+      }
+      const float c = row_scale(ps, rf);
+      // P with the reference as it stands, beside the maximum rather than behind
+      // it; only a page that passes the reference by kSlack (rare after the first
+      // ones) is done again
+      float sum;
+      while (true) {
+        sum = page_weights(sv, c, page_addend(ps, m), pw);
+        const float mx = page_max(sv);
+        const float tm = mx == -INFINITY || ps.vinv == 0.f ? -INFINITY : fmaf(mx, c, ps.ev);
+        if (!__any_sync(0xffffffffu, tm > m + kSlack)) break;
+        const float up = tm > m + kSlack ? ceilf(tm) : m;
+        const float k = up == m || m == -INFINITY ? 1.f : ex2_approx(m - up);
+        if (p > 0) {  // O follows, once the PV of the page before is complete
+          ok = chunk_wait<1>(&sm.pv_done[x][(p - 1) & 1], ((p - 1) >> 1) & 1, abort_flag, st, kSiteCPv, blockIdx.x);
+          if (!ok) break;
+          tc_fence_after();
+          scale_o<D>(colO, k);
+        }
+        l *= k;
+        m = up;
+      }
+      if (!ok) break;
+      l = fmaf(sum, ps.vinv, l);
+      tmem_st32_wait(col, pw);
       tc_fence_before();
       __syncwarp();
-      if (lane == 0) mbar_arrive(&sm.p_full[x]);
+      if (lane == 0) mbar_arrive(&sm.p_full[x][p & 1]);
     }
-    if (ok && T > 0) {
-      ok = chunk_wait<1>(&sm.pv_done[x], (T - 1) & 1, abort_flag, st, kSiteCPv, blockIdx.x);
+    if (ok && P > 0) {
+      ok = chunk_wait<1>(&sm.pv_done[x][(P - 1) & 1], ((P - 1) >> 1) & 1, abort_flag, st, kSiteCPv, blockIdx.x);
       tc_fence_after();
     }
     if (ok) {
-      // ---- the row's result, or its part
+      // ---- the row's result, or its part. A warp's 32 rows go through its
+      // quarter of the Q tile (its last QK is complete) 64 columns at a time, so
+      // that the stores run along rows, a few lines each.
       const bool part = a.splits > 1;
       const float inv = part ? 1.f : (l != 0.f ? 1.f / l : 0.f);
       const long long pr = partial_row(a, b, h, qi, split);
       uint16_t* dst = a.out + b * a.ost.b + h * a.ost.h + static_cast<long long>(qi) * a.ost.n;
+      uint8_t* stage = sm.q[x] + wq * 32 * D * 2;  // 8 KB (D = 128) or 4 KB
+      constexpr int COLS = D / 2;                  // columns per pass: 32 rows of COLS floats, or D of 16 bits
 #pragma unroll 1
-      for (int ch = 0; ch < D / 16; ++ch) {
-        uint32_t o[16];
-        if (T > 0) {
-          tmem_ld16_wait(colO + ch * 16, o);
+      for (int half = 0; half < 2; ++half) {
+        uint32_t o[COLS];
+        if (P > 0) {
+          if constexpr (D == 128) tmem_ld32x2_wait(colO + half * 64, colO + half * 64 + 32, o);
+          else tmem_ld32_wait(colO + half * 32, o);
         } else {
 #pragma unroll
-          for (int e = 0; e < 16; ++e) o[e] = 0;
+          for (int e = 0; e < COLS; ++e) o[e] = 0;
         }
-        if (there && part) {
-          float4* d4 = reinterpret_cast<float4*>(a.part_o + pr * D + ch * 16);
+        if (part) {
 #pragma unroll
-          for (int e = 0; e < 4; ++e)
-            d4[e] = make_float4(__uint_as_float(o[4 * e]), __uint_as_float(o[4 * e + 1]),
-                                __uint_as_float(o[4 * e + 2]), __uint_as_float(o[4 * e + 3]));
-        } else if (there) {
-          uint32_t pk[8];
+          for (int e = 0; e < COLS / 4; ++e)
+            st_shared_v4(stage + (lane * (COLS / 4) + ((e + lane) % (COLS / 4))) * 16, o[4 * e], o[4 * e + 1], o[4 * e + 2],
+                         o[4 * e + 3]);
+        } else {
 #pragma unroll
-          for (int e = 0; e < 8; ++e)
-            pk[e] = pack2<Elem>(__uint_as_float(o[2 * e]) * inv, __uint_as_float(o[2 * e + 1]) * inv);
-          uint4* d4 = reinterpret_cast<uint4*>(dst + ch * 16);
-          d4[0] = make_uint4(pk[0], pk[1], pk[2], pk[3]);
-          d4[1] = make_uint4(pk[4], pk[5], pk[6], pk[7]);
+          for (int e = 0; e < COLS / 8; ++e) {
+            uint32_t pk[4];
+#pragma unroll
+            for (int z = 0; z < 4; ++z)
+              pk[z] = pack2<Elem>(__uint_as_float(o[8 * e + 2 * z]) * inv, __uint_as_float(o[8 * e + 2 * z + 1]) * inv);
+            st_shared_v4(stage + (lane * (COLS / 8) + ((e + lane) % (COLS / 8))) * 16, pk[0], pk[1], pk[2], pk[3]);
+          }
         }
         __syncwarp();
+        if (part) store_rows<COLS / 4>(a, stage, b, hk, r - lane, rows, half, split, lane);
+        else store_rows<COLS / 8>(a, stage, b, hk, r - lane, rows, half, split, lane);
       }
       if (there) {
         if (part) a.part_ml[pr] = make_float2(m, l);
@@ -467,7 +566,7 @@ __global__ void __launch_bounds__(kChunkThreads, 1) cache_chunk_kernel(const Cac
               l == 0.f ? -INFINITY : (m - kPBias + log2f(l)) * kLn2C;
       }
       if (there && sm.nan) {  // NaN values among the tokens that only some rows see
-        for (int u = max(t0 * kTileKeys, least / kTileKeys * kTileKeys); u < min(lim, (t0 + T) * kTileKeys); ++u) {
+        for (int u = max(c0 * kPage, least / kPage * kPage); u < min(lim, (c0 + pend) * kPage); ++u) {
           const int page = page_of(a, b, u / kPage);
           if (page < 0) continue;
           const uint8_t* vr = a.v + page * a.page_stride + (static_cast<long long>(hk) * kPage + u % kPage) * D;
@@ -486,7 +585,7 @@ __global__ void __launch_bounds__(kChunkThreads, 1) cache_chunk_kernel(const Cac
   __syncthreads();
   if (warp == 12) {
     tc_fence_after();
-    tmem_dealloc(tmem, 512);
+    tmem_dealloc(*static_cast<volatile uint32_t*>(&sm.tmem_base), 512);
   }
 }
 

@@ -59,6 +59,13 @@ __device__ __forceinline__ Extent extent(const CacheAttnArgs& a, int b, bool rep
   return e;
 }
 
+// Query token and head within its group of a row (token-major).
+__device__ __forceinline__ void row_place(const CacheAttnArgs& a, int r, int* i, int* g) {
+  const uint32_t u = static_cast<uint32_t>(r);
+  *i = static_cast<int>((__umulhi(a.group_mul, u) + u) >> a.group_shift);
+  *g = r - *i * a.group;
+}
+
 // Keys seen by query i of a sequence: all of them, or (causal) those up to its
 // own place, the queries being the sequence's last cnt tokens.
 __device__ __forceinline__ int key_limit(const Extent& e, int causal, int i) {
@@ -67,11 +74,11 @@ __device__ __forceinline__ int key_limit(const Extent& e, int causal, int i) {
   return l < 0 ? 0 : (l > e.len ? e.len : l);
 }
 
-// Two e4m3 values to fp16 (exact).
-__device__ __forceinline__ uint32_t e4m3x2_f16x2(uint32_t v) {
-  uint32_t r;
-  asm("{\n\t.reg .b16 h;\n\tcvt.u16.u32 h, %1;\n\tcvt.rn.f16x2.e4m3x2 %0, h;\n\t}" : "=r"(r) : "r"(v));
-  return r;
+// Four e4m3 values to two fp16 pairs (exact).
+__device__ __forceinline__ void e4m3x4_f16(uint32_t v, uint32_t& lo, uint32_t& hi) {
+  asm("{\n\t.reg .b16 a, b;\n\tmov.b32 {a, b}, %2;\n\tcvt.rn.f16x2.e4m3x2 %0, a;\n\tcvt.rn.f16x2.e4m3x2 %1, b;\n\t}"
+      : "=r"(lo), "=r"(hi)
+      : "r"(v));
 }
 
 // Some byte of w is an e4m3 NaN (0x7f or 0xff).
@@ -134,7 +141,7 @@ __device__ __forceinline__ PageScale page_scale(const CacheAttnArgs& a, float ks
   if (vs != 0.f) {
     s.ck = ks * a.scale_log2;
     s.ev = __log2f(vs);
-    s.vinv = 1.f / vs;
+    s.vinv = ex2_approx(-s.ev);  // a power of two, as append writes it, comes out exactly
   }
   return s;
 }

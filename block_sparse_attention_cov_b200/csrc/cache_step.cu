@@ -197,9 +197,11 @@ __global__ void __launch_bounds__(kWarps * 32, 2) cache_step_kernel(const CacheA
 #pragma unroll
       for (int e = 0; e < 4; ++e) s[nt][e] = 0.f;
 #pragma unroll
-      for (int j = 0; j < D / 16; ++j)
-        mma16816(s[nt], qa[j][0], qa[j][1], qa[j][2], qa[j][3], e4m3x2_f16x2(cur.k[nt][j] & 0xffffu),
-                 e4m3x2_f16x2(cur.k[nt][j] >> 16));
+      for (int j = 0; j < D / 16; ++j) {
+        uint32_t b0, b1;
+        e4m3x4_f16(cur.k[nt][j], b0, b1);
+        mma16816(s[nt], qa[j][0], qa[j][1], qa[j][2], qa[j][3], b0, b1);
+      }
     }
     // scores in log2 units plus log2 of the value scale
     const PageScale ps = page_scale(a, cur.ks, cur.vs);
@@ -265,14 +267,15 @@ __global__ void __launch_bounds__(kWarps * 32, 2) cache_step_kernel(const CacheA
 #pragma unroll
     for (int w = 0; w < D / 32; ++w) {
       // bytes of two tokens side by side: (a0, b0, a1, b1) and (a2, b2, a3, b3)
-      const uint32_t lo0 = __byte_perm(cur.v[0][w], cur.v[1][w], 0x5140);
-      const uint32_t lo1 = __byte_perm(cur.v[0][w], cur.v[1][w], 0x7362);
-      const uint32_t hi0 = __byte_perm(cur.v[2][w], cur.v[3][w], 0x5140);
-      const uint32_t hi1 = __byte_perm(cur.v[2][w], cur.v[3][w], 0x7362);
-      mma16816(o[4 * w], p0, p1, p2, p3, e4m3x2_f16x2(lo0 & 0xffffu), e4m3x2_f16x2(hi0 & 0xffffu));
-      mma16816(o[4 * w + 1], p0, p1, p2, p3, e4m3x2_f16x2(lo0 >> 16), e4m3x2_f16x2(hi0 >> 16));
-      mma16816(o[4 * w + 2], p0, p1, p2, p3, e4m3x2_f16x2(lo1 & 0xffffu), e4m3x2_f16x2(hi1 & 0xffffu));
-      mma16816(o[4 * w + 3], p0, p1, p2, p3, e4m3x2_f16x2(lo1 >> 16), e4m3x2_f16x2(hi1 >> 16));
+#pragma unroll
+      for (int half = 0; half < 2; ++half) {
+        const uint32_t sel = half ? 0x7362 : 0x5140;
+        uint32_t x0, x1, y0, y1;
+        e4m3x4_f16(__byte_perm(cur.v[0][w], cur.v[1][w], sel), x0, x1);
+        e4m3x4_f16(__byte_perm(cur.v[2][w], cur.v[3][w], sel), y0, y1);
+        mma16816(o[4 * w + 2 * half], p0, p1, p2, p3, x0, y0);
+        mma16816(o[4 * w + 2 * half + 1], p0, p1, p2, p3, x1, y1);
+      }
     }
   }
 

@@ -124,6 +124,8 @@ struct CacheAttnArgs {
   float scale_log2;       // softmax scale * log2(e)
   int dtype, pages, columns, B, H, Hk, N, d;
   int group;              // H / Hk
+  uint32_t group_mul;     // row / group = (umulhi(group_mul, row) + row) >> group_shift, row < 2^31
+  uint32_t group_shift;
   int causal;
   int splits;             // parts of the key axis, joined from part_o / part_ml when > 1
   float* part_o;          // [B][H][N][splits][d]
@@ -135,7 +137,7 @@ struct CachePlan {
   bool step;
   int splits;
 };
-CachePlan cache_plan(int B, int H, int Hk, int N, int columns);
+CachePlan cache_plan(int B, int H, int Hk, int N, int d, int columns);
 cudaError_t launch_cache_step(const CacheAttnArgs& a, cudaStream_t stream);
 cudaError_t launch_cache_chunk(const CacheAttnArgs& a, cudaStream_t stream);
 cudaError_t launch_cache_join(const CacheAttnArgs& a, cudaStream_t stream);

@@ -271,7 +271,7 @@ int solattn_cache_workspace_bytes(int B, int H, int N, int d, int H_kv, int colu
   if (!bytes) return SOLATTN_ERR_ARG;
   const int rc = check_attention_shape(B, H, N, d, H_kv, columns);
   if (rc) return rc;
-  *bytes = attention_workspace(B, H, N, d, solattn::cache_plan(B, H, H_kv, N, columns).splits);
+  *bytes = attention_workspace(B, H, N, d, solattn::cache_plan(B, H, H_kv, N, d, columns).splits);
   return SOLATTN_OK;
 }
 
@@ -292,7 +292,7 @@ int solattn_cache_attention(const void* q, int dtype, int B, int H, int N, int d
   if ((rc = tensor_strides(strides, B, H, N, d, false, &a.st))) return rc;
   if ((rc = tensor_strides(out_strides, B, H, N, d, true, &a.ost))) return rc;
   if (!multiple_of_8(a.st) || !multiple_of_8(a.ost)) return SOLATTN_ERR_ARG;
-  const solattn::CachePlan plan = solattn::cache_plan(B, H, cache->heads, N, columns);
+  const solattn::CachePlan plan = solattn::cache_plan(B, H, cache->heads, N, d, columns);
   if (!workspace || workspace_bytes < attention_workspace(B, H, N, d, plan.splits)) return SOLATTN_ERR_WORKSPACE;
   if (!solattn::aligned16(workspace)) return SOLATTN_ERR_ALIGN;
   int sms = 0;
@@ -320,6 +320,8 @@ int solattn_cache_attention(const void* q, int dtype, int B, int H, int N, int d
   a.N = N;
   a.d = d;
   a.group = H / cache->heads;
+  while ((1ll << a.group_shift) < a.group) ++a.group_shift;
+  a.group_mul = static_cast<uint32_t>((1ull << 32) * ((1ull << a.group_shift) - a.group) / a.group + 1);
   a.causal = causal != 0;
   a.splits = plan.splits;
   char* ws = static_cast<char*>(workspace) + SOLATTN_WORKSPACE_BYTES;
@@ -336,7 +338,7 @@ int solattn_cache_attention(const void* q, int dtype, int B, int H, int N, int d
 
 namespace solattn {
 
-CachePlan cache_plan(int B, int H, int Hk, int N, int columns) {
+CachePlan cache_plan(int B, int H, int Hk, int N, int d, int columns) {
   constexpr int kSms = 148;
   const long long rows = static_cast<long long>(N) * (H / Hk);
   CachePlan p{rows <= 64, 1};
@@ -346,9 +348,23 @@ CachePlan cache_plan(int B, int H, int Hk, int N, int columns) {
     // three waves of two CTAs per SM, at least four pages a part
     p.splits = static_cast<int>(std::fmax(1, std::fmin(ceil_div(6 * kSms, units), ceil_div(columns, 4))));
   } else {
-    const long long units = static_cast<long long>(B) * Hk * ceil_div(rows, 256);
-    // one CTA per SM, at least four key tiles (of two pages) a part
-    p.splits = static_cast<int>(std::fmax(1, std::fmin(kSms / units, ceil_div(columns, 8))));
+    // One CTA per SM: a part of the key axis costs about 9 us to start and finish
+    // and 2.5 us per key tile (two pages), parts run in waves of 148, and what is
+    // joined is written and read once at about 6 TB/s. The split with the least
+    // sum is taken (120 CTAs of 591 key tiles, 8 heads of 3600 queries over 75600
+    // keys: 1466 us in one part, 1325 us in 6). With several sequences that fill
+    // the GPU by their upper bounds the key axis stays whole: shorter sequences
+    // leave fewer CTAs than that (3 of up to 1111 queries: 62 us, 95 us in 2).
+    const long long units = static_cast<long long>(B) * Hk * ceil_div(rows, 256), tiles = ceil_div(columns, 2);
+    double best = 0;
+    for (int s = 1; s <= 16 && (s == 1 || (s * 2 <= tiles && (B == 1 || units < kSms))); ++s) {
+      const double join = s == 1 ? 0 : 3 + static_cast<double>(B) * H * N * s * d * 8 / 6e6;
+      const double cost = ceil_div(units * s, kSms) * (9 + 2.5 * ceil_div(tiles, s)) + join;
+      if (s == 1 || cost < best) {
+        best = cost;
+        p.splits = s;
+      }
+    }
   }
   return p;
 }

@@ -335,6 +335,45 @@ def test_append_extremes():
     assert float(c.k_scale[1, 0]) == 2.0 ** 32
 
 
+@pytest.mark.parametrize("N", [1, 80])
+@pytest.mark.parametrize("d", [64, 128])
+def test_every_e4m3_value_is_read_exactly(N, d):
+    """One key of every e4m3 value, subnormals and both signs, among otherwise zero keys: the outputs of queries that pick
+    single dimensions are those values' softmax, and values come back as they are where one key takes all."""
+    codes = torch.tensor([b for b in range(256) if b & 0x7F != 0x7F], dtype=torch.uint8)
+    n = codes.numel()  # 254 tokens
+    c = sa.Cache.empty(4, 1, d)
+    c.k.view(torch.uint8).zero_(), c.v.view(torch.uint8).zero_()
+    c.k_scale.fill_(1.0), c.v_scale.fill_(2.0 ** 5)
+    flat_k, flat_v = c.k.view(torch.uint8).view(256, d), c.v.view(torch.uint8).view(256, d)
+    for j in range(d):  # dimension j of token u holds code (u + 7 j)
+        flat_v[:n, j] = codes.roll(-7 * j).cuda()
+    marks = torch.randperm(n, generator=_gen(70))[:N]
+    t = torch.arange(4, dtype=torch.int32).view(1, 4)
+    for i, u in enumerate(marks.tolist()):  # key u alone has 448 in dimension i % d, and wins by far
+        if i < d:
+            flat_k[u, i] = 0x7E
+    rows = min(N, d)
+    q = torch.zeros((1, 1, N, d), dtype=torch.bfloat16)
+    for i in range(rows):
+        q[0, 0, i, i] = 8.0
+    out, lse = sa.cache_attention(q.cuda(), c, t.cuda(), _i32([n]), causal=False)
+    for i, u in enumerate(marks.tolist()[:rows]):
+        want = flat_v[u].view(E4M3).double().cpu() * 32
+        # the other 253 keys weigh e^-(448 * 8 / sqrt(d)) each: nothing
+        assert torch.equal(out[0, 0, i].double().cpu(), want.to(torch.bfloat16).double())
+    # keys: scores of every code through lse of two keys, the code's and a zero
+    for code in (0x01, 0x07, 0x08, 0x81, 0x3C, 0x7E, 0xFE):
+        flat_k.zero_()
+        flat_k[0, 5] = code
+        q = torch.zeros((1, 1, N, d), dtype=torch.bfloat16)
+        q[..., 5] = 1.0
+        value = float(torch.tensor([code], dtype=torch.uint8).view(E4M3).float())
+        scale = 4.0 if abs(value) < 1 else 0.01
+        _, lse = sa.cache_attention(q.cuda(), c, t.cuda(), _i32([1]), causal=False, scale=scale)
+        assert torch.allclose(lse.cpu(), torch.full_like(lse.cpu(), value * scale), rtol=2.0 ** -20, atol=2.0 ** -20)
+
+
 def test_token_by_token_equals_a_chunk_where_scales_agree():
     """Appending one by one ends with the scale of the whole page, and with its bytes save values that sank."""
     d, n = 128, 64
