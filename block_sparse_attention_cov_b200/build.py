@@ -19,7 +19,7 @@ LIB = os.path.join(PKG, "libsolattn.so")
 LIB_HOOKS = os.path.join(PKG, "libsolattn_testhooks.so")
 SOURCES = ["api.cu", "ops_api.cu", "pool.cu", "forward.cu", "forward_pp.cu", "rotary.cu", "cache_append.cu",
            "cache_step.cu", "cache_chunk.cu"]
-HEADERS = ["kernels.h", "api_common.h", "ptx.cuh", "fwd_common.cuh", "cache_common.cuh"]
+HEADERS = ["kernels.h", "api_common.h", "ptx.cuh", "fwd_common.cuh", "cache_common.cuh", "tensor_map.h"]
 
 NVCC_FLAGS = [
     "-gencode", "arch=compute_100a,code=sm_100a",

@@ -233,6 +233,7 @@ __global__ void __launch_bounds__(kChunkThreads, 1) cache_chunk_kernel(const Cac
   const int hk = blockIdx.y, b = blockIdx.z;
   DeviceStatus* st = a.status;
   volatile int* abort_flag = &sm.abort_flag;
+  start_join(a);
   if (tid == 0) {
     for (int i = 0; i < kKStages; ++i) {
       mbar_init(&sm.k_full[i], 8);  // four warps, two pages

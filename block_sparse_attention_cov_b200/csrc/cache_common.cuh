@@ -81,6 +81,12 @@ __device__ __forceinline__ void e4m3x4_f16(uint32_t v, uint32_t& lo, uint32_t& h
       : "r"(v));
 }
 
+// Lets the joining kernel of a split call set itself up; it waits for this
+// kernel's end before it reads a part.
+__device__ __forceinline__ void start_join(const CacheAttnArgs& a) {
+  if (a.splits > 1) asm volatile("griddepcontrol.launch_dependents;");
+}
+
 // Some byte of w is an e4m3 NaN (0x7f or 0xff).
 __device__ __forceinline__ bool has_nan8(uint32_t w) {
   return (((w & 0x7f7f7f7fu) + 0x01010101u) & 0x80808080u) != 0;

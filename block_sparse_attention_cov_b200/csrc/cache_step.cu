@@ -3,17 +3,20 @@
 //
 // cache_step_kernel is bound by reading the cache: 2 d bytes per key and head
 // against 4 d flops per query row. One CTA takes up to 16 rows (query heads of
-// one key head x new tokens) and one part of the sequence's pages; its four
-// warps take 16 of a page's 64 tokens each and keep their own running softmax,
-// joined at the end. The next page's keys and values are in flight, in
-// registers, while a page is multiplied: fragments are loaded straight from the
-// cache with 16-byte loads, which works because the order of the contracted
-// index is free as long as both operands agree on it:
-//   S = Q K^T: lane (g, t) holds bytes 16t.. of token g's row; word j of them is
+// one key head x new tokens) and one part of the sequence's pages. A producer
+// warp keeps four pages of keys and values on their way into shared memory by TMA
+// (64 KB per CTA, three CTAs per SM; with one page ahead in registers the kernel
+// waited for memory at 4.1 TB/s); four warps take 32 tokens each, half of every
+// other page, and keep their own running softmax, joined at the end. Fragments come from
+// shared memory with 16-byte loads, which works because the order of the
+// contracted index is free as long as both operands agree on it:
+//   S = Q K^T: lane (g, t) holds bytes 16t.. of one token's row; word j of them is
 //     the fragment of contraction step j, and Q is loaded in the same order;
 //   O = P V: the softmax's accumulator layout is the A fragment of P; lane (g, t)
-//     holds bytes 16g.. of tokens 2t, 2t+1, 2t+8, 2t+9, byte permutes pair the
-//     tokens, and byte j is column j of value tile j: 16 tiles of 8 columns.
+//     holds bytes 16g.. of the four tokens whose weights it has, byte permutes
+//     pair the tokens, and byte j is column j of value tile j.
+// Column n of a score tile is token n, or n ^ 4 where n is odd: with the 128-byte
+// swizzle neither operand's loads meet in a bank.
 // The products run on mma.sync (m16n8k16, fp16 operands, fp32 sums): a 16-row
 // tile is what these calls have, a tcgen05 tile would be 7/8 empty, and at 16
 // rows the tensor pipe is far from the bound.
@@ -22,6 +25,7 @@
 #include <cstdint>
 
 #include "cache_common.cuh"
+#include "tensor_map.h"
 
 namespace solattn {
 
@@ -29,6 +33,8 @@ namespace {
 
 constexpr int kRows = 16;   // rows per CTA
 constexpr int kWarps = 4;
+
+enum : uint32_t { kSiteStepFull = 60, kSiteStepEmpty };
 
 __device__ __forceinline__ void mma16816(float (&c)[4], const uint32_t a0, const uint32_t a1, const uint32_t a2,
                                          const uint32_t a3, const uint32_t b0, const uint32_t b1) {
@@ -38,68 +44,151 @@ __device__ __forceinline__ void mma16816(float (&c)[4], const uint32_t a0, const
       : "r"(a0), "r"(a1), "r"(a2), "r"(a3), "r"(b0), "r"(b1));
 }
 
-__device__ __forceinline__ uint4 ld_cache(const uint8_t* p) {
-  uint4 r;
-  asm volatile("ld.global.nc.L1::no_allocate.v4.u32 {%0,%1,%2,%3}, [%4];"
-               : "=r"(r.x), "=r"(r.y), "=r"(r.z), "=r"(r.w)
-               : "l"(p));
-  return r;
-}
-__device__ __forceinline__ uint2 ld_cache8(const uint8_t* p) {
-  uint2 r;
-  asm volatile("ld.global.nc.L1::no_allocate.v2.u32 {%0,%1}, [%2];" : "=r"(r.x), "=r"(r.y) : "l"(p));
-  return r;
-}
-
-// One warp's 16 tokens of a page, as loaded.
 template <int D>
-struct Tokens {
-  uint32_t k[2][D / 16];  // token 8 nt + g: bytes 16t.. (and 64 + 16t.. at D = 128)
-  uint32_t v[4][D / 32];  // tokens 2t, 2t+1, 2t+8, 2t+9: bytes (D/8) g ..
-  float ks, vs;           // the page's scales; vs = 0: the page is not there
+struct __align__(1024) StepSmem {
+  static constexpr int kStages = 4;
+  union {
+    struct {
+      uint8_t k[kStages][kPage * D];  // 128-byte rows (64 at D = 64), swizzled as wide
+      uint8_t v[kStages][kPage * D];
+    };
+    struct {  // the warps' results, when every page is done
+      float o[kWarps][kRows][D + 4];
+      float m[kWarps][kRows];
+      float l[kWarps][kRows];
+    };
+  };
+  uint4 q[D / 16][32];    // Q fragments of step j, by lane
+  float2 scale[kStages];  // of keys and values; 0 values: the page is not there
+  uint64_t full[kStages], empty[kStages];
+  int nan;  // a value that only some rows see is NaN
+  int abort_flag;
 };
 
+// Offset of 16-byte chunk c of row r: the TMA swizzle of rows of D bytes.
 template <int D>
-struct StepSmem {
-  float o[kWarps][kRows][D + 4];
-  float m[kWarps][kRows];
-  float l[kWarps][kRows];
-  int nan;  // a value of the causal zone is NaN
-};
+__device__ __forceinline__ uint32_t swizzled(int r, int c) {
+  return D == 128 ? r * 128 + ((c ^ (r & 7)) << 4) : r * 64 + ((c ^ ((r >> 1) & 3)) << 4);
+}
 
 template <typename T, int D>
-__global__ void __launch_bounds__(kWarps * 32, 2) cache_step_kernel(const CacheAttnArgs a) {
-  __shared__ StepSmem<D> sm;
+__global__ void __launch_bounds__((kWarps + 1) * 32, 3)
+    cache_step_kernel(const __grid_constant__ CUtensorMap tmK, const __grid_constant__ CUtensorMap tmV,
+                      const CacheAttnArgs a) {
+  using Smem = StepSmem<D>;
+  constexpr int ST = Smem::kStages;
+  extern __shared__ uint8_t smem_raw[];
+  Smem& sm = *reinterpret_cast<Smem*>(smem_raw + ((1024u - (smem_u32(smem_raw) & 1023u)) & 1023u));
   const int tid = threadIdx.x, warp = tid / 32, lane = tid % 32;
   const int g = lane / 4, t = lane % 4;
   const int split = blockIdx.x, b = blockIdx.z;
   const int hk = blockIdx.y % a.Hk, tile = blockIdx.y / a.Hk;
+  DeviceStatus* st = a.status;
+  volatile int* abort_flag = &sm.abort_flag;
+  start_join(a);
+  if (tid == 0) {
+    for (int i = 0; i < ST; ++i) {
+      mbar_init(&sm.full[i], 2);  // the copies' issue and the scales
+      mbar_init(&sm.empty[i], 2);  // two warps share a page
+    }
+    sm.nan = 0;
+    sm.abort_flag = 0;
+    fence_barrier_init();
+  }
+  __syncthreads();
   const Extent ex = extent(a, b, split == 0 && hk == 0 && tile == 0 && tid == 0);
   const int rows = ex.cnt * a.group;
   const int r0 = tile * kRows;
   if (r0 >= rows) return;  // rows behind the sequence's queries stay as they are
-  if (tid == 0) sm.nan = 0;
-  __syncthreads();
 
   // the CTA's pages: its split's share of those that its last row sees
-  const int last_row = min(rows, r0 + kRows) - 1;
-  const int seen = key_limit(ex, a.causal, last_row / a.group);
+  int qi, qg;
+  row_place(a, min(rows, r0 + kRows) - 1, &qi, &qg);
+  const int seen = key_limit(ex, a.causal, qi);
   const int pages = (seen + kPage - 1) / kPage;
   const int per = (pages + a.splits - 1) / a.splits;
   const int c0 = min(pages, split * per), c1 = min(pages, c0 + per);
+  row_place(a, r0, &qi, &qg);
+  const int lim_all = key_limit(ex, a.causal, qi);  // row r0 sees least
+  const bool zone_rows = a.causal && ex.cnt > 1;
 
-  // Q fragments of rows g and g + 8, scaled to fp16's range
-  uint32_t qa[D / 16][4];
+  if (warp == kWarps) {
+    // ======================= producer =======================
+    const int32_t* table = a.table + b * a.table_stride;
+    if (lane == 0) {
+      prefetch_tensormap(&tmK);
+      prefetch_tensormap(&tmV);
+    }
+    bool ok = true;
+    int issued = 0;
+    for (int base = c0; base < c1 && ok; base += 32) {
+      // 32 pages' numbers and scales at once
+      int pg = -1;
+      float ks = 0.f, vs = 0.f;
+      if (base + lane < c1) {
+        pg = __ldg(table + base + lane);
+        if (pg < 0 || pg >= a.pages) {
+          report_page(st, b);
+          pg = -1;
+        } else {
+          ks = __ldg(a.k_scale + pg * a.scale_stride + hk);
+          vs = __ldg(a.v_scale + pg * a.scale_stride + hk);
+        }
+      }
+      const int count = min(32, c1 - base);
+      // the first pages' copies go out before their scales have come
+      const int ahead = base == c0 ? min(count, ST) : 0;
+      auto issue = [&](int n, int page) {
+        if (lane == 0) {
+          const int s = n % ST;
+          if (page >= 0) {
+            mbar_arrive_expect_tx(&sm.full[s], 2 * kPage * D);
+            tma_load_4d(sm.k[s], &tmK, &sm.full[s], 0, 0, hk, page);
+            tma_load_4d(sm.v[s], &tmV, &sm.full[s], 0, 0, hk, page);
+          } else {
+            mbar_arrive(&sm.full[s]);
+          }
+        }
+        issued = n + 1;
+      };
+      for (int i = 0; i < ahead; ++i) issue(i, __shfl_sync(0xffffffffu, pg, i));
+      for (int i = 0; i < count && ok; ++i) {
+        const int n = base + i - c0, s = n % ST;
+        const int page = __shfl_sync(0xffffffffu, pg, i);
+        if (i >= ahead) {
+          if (n >= ST)
+            ok = __all_sync(0xffffffffu, mbar_wait(&sm.empty[s], ((n / ST) & 1) ^ 1, abort_flag, st, kSiteStepEmpty,
+                                                   blockIdx.x));
+          if (!ok) break;
+          issue(n, page);
+        }
+        const float2 kv = make_float2(__shfl_sync(0xffffffffu, ks, i), __shfl_sync(0xffffffffu, vs, i));
+        if (lane == 0) {
+          sm.scale[s] = kv;
+          mbar_arrive(&sm.full[s]);
+        }
+      }
+    }
+    if (!ok && lane == 0)  // teardown after a wait that gave up: issued copies land before the block exits
+      for (int n = max(0, issued - ST); n < issued; ++n) mbar_wait_quiet(&sm.full[n % ST], (n / ST) & 1);
+    __syncwarp();
+    __syncthreads();  // with the warps' results
+    return;
+  }
+
+  // ======================= four warps =======================
+  // Q fragments of rows g and g + 8, scaled to fp16's range, in shared memory: in
+  // registers they would cost the third block of an SM
   float rf[2];
   int lim[2];
 #pragma unroll
   for (int x = 0; x < 2; ++x) {
     const int r = r0 + g + 8 * x;
-    const int i = r / a.group, h = hk * a.group + r % a.group;
+    row_place(a, r, &qi, &qg);
     const bool there = r < rows;
-    lim[x] = there ? key_limit(ex, a.causal, i) : 0;
+    lim[x] = there ? key_limit(ex, a.causal, qi) : 0;
     uint4 w[D / 32];
-    const uint16_t* src = a.q + b * a.st.b + h * a.st.h + static_cast<long long>(i) * a.st.n;
+    const uint16_t* src = a.q + b * a.st.b + (hk * a.group + qg) * a.st.h + static_cast<long long>(qi) * a.st.n;
 #pragma unroll
     for (int y = 0; y < D / 32; ++y)  // 16 dims at 16t (+ 64) as two chunks of 8
       w[y] = there ? *reinterpret_cast<const uint4*>(src + (y / 2) * 64 + 16 * t + (y % 2) * 8) : make_uint4(0, 0, 0, 0);
@@ -123,12 +212,12 @@ __global__ void __launch_bounds__(kWarps * 32, 2) cache_step_kernel(const CacheA
 #pragma unroll
       for (int e = 0; e < 4; ++e) {  // two dims each; step (4 dims) 2 y + e / 2
         const float2 f = unpack2<T>(u[e]);
-        qa[2 * y + e / 2][(e & 1) * 2 + x] = pack_f16x2(f.x * mul, f.y * mul);
+        if (warp == 0)
+          reinterpret_cast<uint32_t*>(&sm.q[2 * y + e / 2][lane])[(e & 1) * 2 + x] = pack_f16x2(f.x * mul, f.y * mul);
       }
     }
   }
-  const int lim_all = min(__shfl_sync(0xffffffffu, lim[0], 0), ex.len);  // row r0 sees least
-  const bool zone_rows = a.causal && ex.cnt > 1;
+  named_bar_sync(1, kWarps * 32);
 
   float o[D / 8][4];
 #pragma unroll
@@ -137,149 +226,152 @@ __global__ void __launch_bounds__(kWarps * 32, 2) cache_step_kernel(const CacheA
     for (int e = 0; e < 4; ++e) o[j][e] = 0.f;
   float m[2] = {-INFINITY, -INFINITY}, l[2] = {0.f, 0.f};
 
-  const uint8_t* kb = a.k + static_cast<long long>(hk) * kPage * D + (warp * 16 + g) * D + 16 * t;
-  const uint8_t* vb = a.v + static_cast<long long>(hk) * kPage * D + (warp * 16 + 2 * t) * D + (D / 8) * g;
-  // Issues a page's loads; nothing here waits for one.
-  auto fetch = [&](Tokens<D>& x, int col, int page) {
-    const bool there = page >= 0 && page < a.pages;
-    if (!there) report_page(a.status, b);
-    const long long at = there ? page * a.page_stride : 0;
-    x.ks = there ? __ldg(a.k_scale + page * a.scale_stride + hk) : 0.f;
-    x.vs = there ? __ldg(a.v_scale + page * a.scale_stride + hk) : 0.f;
+  // A warp takes half of every other page, 32 tokens at a time: two groups of 16,
+  // whose products are independent. Token of score column n, and the lane's four
+  // tokens of a group:
+  const int first = (warp & 1) * 32, kr = (g & 1) ? g ^ 4 : g;
+  const int tok[4] = {2 * t, (2 * t + 1) ^ 4, 8 + 2 * t, 8 + ((2 * t + 1) ^ 4)};
+  bool ok = true;
+  for (int col = c0 + warp / 2; col < c1; col += 2) {
+    const int n = col - c0, s = n % ST;
+    ok = __all_sync(0xffffffffu, mbar_wait(&sm.full[s], (n / ST) & 1, abort_flag, st, kSiteStepFull, blockIdx.x));
+    if (!ok) break;
+    const int base = col * kPage + first;
+    if (base < seen) {  // warp-uniform
+      const float2 kv = sm.scale[s];
+      const bool gone = kv.y == 0.f;
+      float sc[4][4];
 #pragma unroll
-    for (int nt = 0; nt < 2; ++nt) {
+      for (int nt = 0; nt < 4; ++nt)
+#pragma unroll
+        for (int e = 0; e < 4; ++e) sc[nt][e] = 0.f;
 #pragma unroll
       for (int y = 0; y < D / 64; ++y) {
-        const uint4 w = there ? ld_cache(kb + at + nt * 8 * D + y * 64) : make_uint4(0, 0, 0, 0);
-        x.k[nt][4 * y] = w.x;
-        x.k[nt][4 * y + 1] = w.y;
-        x.k[nt][4 * y + 2] = w.z;
-        x.k[nt][4 * y + 3] = w.w;
-      }
-    }
-    const int pos = col * kPage + warp * 16 + 2 * t;  // of the lane's first token
+        uint4 kw[4];
 #pragma unroll
-    for (int y = 0; y < 4; ++y) {
-      const int off = (y & 1) + (y >> 1) * 8;
-      // rows behind the sequence hold anything, NaN too: zero weights do not
-      // silence it in the product
-      const bool in = there && pos + off < ex.len;
-      if constexpr (D == 128) {
-        const uint4 w = in ? ld_cache(vb + at + off * D) : make_uint4(0, 0, 0, 0);
-        x.v[y][0] = w.x;
-        x.v[y][1] = w.y;
-        x.v[y][2] = w.z;
-        x.v[y][3] = w.w;
-      } else {
-        const uint2 w = in ? ld_cache8(vb + at + off * D) : make_uint2(0, 0);
-        x.v[y][0] = w.x;
-        x.v[y][1] = w.y;
-      }
-    }
-  };
-
-  const int32_t* table = a.table + b * a.table_stride;
-  Tokens<D> nxt;
-  int page = 0;  // of column col + 1, loaded one trip ahead of the page itself
-  if (c0 < c1) {
-    fetch(nxt, c0, __ldg(table + c0));
-    if (c0 + 1 < c1) page = __ldg(table + c0 + 1);
-  }
-  for (int col = c0; col < c1; ++col) {
-    Tokens<D> cur = nxt;
-    if (col + 1 < c1) fetch(nxt, col + 1, page);
-    if (col + 2 < c1) page = __ldg(table + col + 2);
-    const int base = col * kPage + warp * 16;
-    if (base >= seen) continue;  // warp-uniform
-    float s[2][4];
+        for (int nt = 0; nt < 4; ++nt)
+          kw[nt] = gone ? make_uint4(0, 0, 0, 0)
+                        : *reinterpret_cast<const uint4*>(sm.k[s] + swizzled<D>(first + 8 * nt + kr, t + 4 * y));
 #pragma unroll
-    for (int nt = 0; nt < 2; ++nt) {
+        for (int j = 0; j < 4; ++j) {
+          const uint4 qf = sm.q[4 * y + j][lane];
 #pragma unroll
-      for (int e = 0; e < 4; ++e) s[nt][e] = 0.f;
-#pragma unroll
-      for (int j = 0; j < D / 16; ++j) {
-        uint32_t b0, b1;
-        e4m3x4_f16(cur.k[nt][j], b0, b1);
-        mma16816(s[nt], qa[j][0], qa[j][1], qa[j][2], qa[j][3], b0, b1);
-      }
-    }
-    // scores in log2 units plus log2 of the value scale
-    const PageScale ps = page_scale(a, cur.ks, cur.vs);
-    const float c[2] = {ps.ck * rf[0], ps.ck * rf[1]};
-#pragma unroll
-    for (int nt = 0; nt < 2; ++nt)
-#pragma unroll
-      for (int e = 0; e < 4; ++e) s[nt][e] = fmaf(s[nt][e], c[e >> 1], ps.ev);
-    if (base + 16 > lim_all) {
-#pragma unroll
-      for (int nt = 0; nt < 2; ++nt)
-#pragma unroll
-        for (int e = 0; e < 4; ++e)
-          if (base + nt * 8 + 2 * t + (e & 1) >= lim[e >> 1]) s[nt][e] = -INFINITY;
-      if (zone_rows) {  // a NaN value must reach only the rows that see its token
-        bool bad = false;
-#pragma unroll
-        for (int y = 0; y < 4; ++y)
-#pragma unroll
-          for (int w = 0; w < D / 32; ++w) {
-            bad |= has_nan8(cur.v[y][w]);
-            cur.v[y][w] = drop_nan8(cur.v[y][w]);
+          for (int nt = 0; nt < 4; ++nt) {
+            uint32_t b0, b1;
+            e4m3x4_f16(j == 0 ? kw[nt].x : (j == 1 ? kw[nt].y : (j == 2 ? kw[nt].z : kw[nt].w)), b0, b1);
+            mma16816(sc[nt], qf.x, qf.y, qf.z, qf.w, b0, b1);
           }
-        if (bad) sm.nan = 1;
+        }
       }
-    }
-    float mx[2];
-    bool raise = false;
+      // scores in log2 units plus log2 of the value scale
+      const PageScale ps = page_scale(a, kv.x, kv.y);
+      const float c[2] = {ps.ck * rf[0], ps.ck * rf[1]};
 #pragma unroll
-    for (int x = 0; x < 2; ++x) {
-      mx[x] = fmaxf(fmaxf(s[0][2 * x], s[0][2 * x + 1]), fmaxf(s[1][2 * x], s[1][2 * x + 1]));
-      mx[x] = fmaxf(mx[x], __shfl_xor_sync(0xffffffffu, mx[x], 1));
-      mx[x] = fmaxf(mx[x], __shfl_xor_sync(0xffffffffu, mx[x], 2));
-      raise |= mx[x] > m[x] + kSlack;
-    }
-    if (__any_sync(0xffffffffu, raise)) {
+      for (int nt = 0; nt < 4; ++nt)
+#pragma unroll
+        for (int e = 0; e < 4; ++e) sc[nt][e] = fmaf(sc[nt][e], c[e >> 1], ps.ev);
+      const bool zone = base + 32 > lim_all;
+      if (zone) {
+#pragma unroll
+        for (int nt = 0; nt < 4; ++nt)
+#pragma unroll
+          for (int e = 0; e < 4; ++e)
+            if (base + 16 * (nt / 2) + tok[2 * (nt & 1) + (e & 1)] >= lim[e >> 1]) sc[nt][e] = -INFINITY;
+      }
+      float mx[2];
+      bool raise = false;
 #pragma unroll
       for (int x = 0; x < 2; ++x) {
-        const float mn = mx[x] > m[x] + kSlack ? ceilf(mx[x]) : m[x];
-        const float k = m[x] == mn ? 1.f : ex2_approx(m[x] - mn);  // 0 from -inf
-        l[x] *= k;
+        mx[x] = -INFINITY;
 #pragma unroll
-        for (int j = 0; j < D / 8; ++j) {
-          o[j][2 * x] *= k;
-          o[j][2 * x + 1] *= k;
+        for (int nt = 0; nt < 4; ++nt) mx[x] = fmaxf(mx[x], fmaxf(sc[nt][2 * x], sc[nt][2 * x + 1]));
+        mx[x] = fmaxf(mx[x], __shfl_xor_sync(0xffffffffu, mx[x], 1));
+        mx[x] = fmaxf(mx[x], __shfl_xor_sync(0xffffffffu, mx[x], 2));
+        raise |= mx[x] > m[x] + kSlack;
+      }
+      if (__any_sync(0xffffffffu, raise)) {
+#pragma unroll
+        for (int x = 0; x < 2; ++x) {
+          const float mn = mx[x] > m[x] + kSlack ? ceilf(mx[x]) : m[x];
+          const float k = m[x] == mn ? 1.f : ex2_approx(m[x] - mn);  // 0 from -inf
+          l[x] *= k;
+#pragma unroll
+          for (int j = 0; j < D / 8; ++j) {
+            o[j][2 * x] *= k;
+            o[j][2 * x + 1] *= k;
+          }
+          m[x] = mn;
         }
-        m[x] = mn;
+      }
+      float sum[2] = {0.f, 0.f};
+      const float sub[2] = {kPBias - (m[0] == -INFINITY ? 0.f : m[0]), kPBias - (m[1] == -INFINITY ? 0.f : m[1])};
+#pragma unroll
+      for (int nt = 0; nt < 4; ++nt)
+#pragma unroll
+        for (int e = 0; e < 4; ++e) {
+          sc[nt][e] = ex2_approx(sc[nt][e] + sub[e >> 1]);
+          sum[e >> 1] += sc[nt][e];
+        }
+      l[0] = fmaf(sum[0], ps.vinv, l[0]);
+      l[1] = fmaf(sum[1], ps.vinv, l[1]);
+#pragma unroll
+      for (int grp = 0; grp < 2; ++grp) {
+        uint32_t vw[4][D / 32];
+#pragma unroll
+        for (int y = 0; y < 4; ++y) {
+          // rows behind the sequence hold anything, NaN too: zero weights do not
+          // silence it in the product
+          const int r = first + 16 * grp + tok[y];
+          const bool in = !gone && col * kPage + r < ex.len;
+          if constexpr (D == 128) {
+            const uint4 w = in ? *reinterpret_cast<const uint4*>(sm.v[s] + swizzled<D>(r, g)) : make_uint4(0, 0, 0, 0);
+            vw[y][0] = w.x;
+            vw[y][1] = w.y;
+            vw[y][2] = w.z;
+            vw[y][3] = w.w;
+          } else {
+            const uint2 w = in ? *reinterpret_cast<const uint2*>(sm.v[s] + swizzled<D>(r, g / 2) + 8 * (g & 1))
+                               : make_uint2(0, 0);
+            vw[y][0] = w.x;
+            vw[y][1] = w.y;
+          }
+        }
+        if (zone && zone_rows) {  // a NaN value must reach only the rows that see its token
+          bool bad = false;
+#pragma unroll
+          for (int y = 0; y < 4; ++y)
+#pragma unroll
+            for (int w = 0; w < D / 32; ++w) {
+              bad |= has_nan8(vw[y][w]);
+              vw[y][w] = drop_nan8(vw[y][w]);
+            }
+          if (bad) sm.nan = 1;
+        }
+        const float(&q0)[4] = sc[2 * grp];
+        const float(&q1)[4] = sc[2 * grp + 1];
+        const uint32_t p0 = pack_f16x2(q0[0], q0[1]), p1 = pack_f16x2(q0[2], q0[3]);
+        const uint32_t p2 = pack_f16x2(q1[0], q1[1]), p3 = pack_f16x2(q1[2], q1[3]);
+#pragma unroll
+        for (int w = 0; w < D / 32; ++w) {
+          // bytes of two tokens side by side: (a0, b0, a1, b1) and (a2, b2, a3, b3)
+#pragma unroll
+          for (int half = 0; half < 2; ++half) {
+            const uint32_t sel = half ? 0x7362 : 0x5140;
+            uint32_t x0, x1, y0, y1;
+            e4m3x4_f16(__byte_perm(vw[0][w], vw[1][w], sel), x0, x1);
+            e4m3x4_f16(__byte_perm(vw[2][w], vw[3][w], sel), y0, y1);
+            mma16816(o[4 * w + 2 * half], p0, p1, p2, p3, x0, y0);
+            mma16816(o[4 * w + 2 * half + 1], p0, p1, p2, p3, x1, y1);
+          }
+        }
       }
     }
-    float sum[2] = {0.f, 0.f};
-#pragma unroll
-    for (int nt = 0; nt < 2; ++nt)
-#pragma unroll
-      for (int e = 0; e < 4; ++e) {
-        const float mr = m[e >> 1] == -INFINITY ? 0.f : m[e >> 1];
-        s[nt][e] = ex2_approx(s[nt][e] - mr + kPBias);
-        sum[e >> 1] += s[nt][e];
-      }
-    l[0] = fmaf(sum[0], ps.vinv, l[0]);
-    l[1] = fmaf(sum[1], ps.vinv, l[1]);
-    const uint32_t p0 = pack_f16x2(s[0][0], s[0][1]), p1 = pack_f16x2(s[0][2], s[0][3]);
-    const uint32_t p2 = pack_f16x2(s[1][0], s[1][1]), p3 = pack_f16x2(s[1][2], s[1][3]);
-#pragma unroll
-    for (int w = 0; w < D / 32; ++w) {
-      // bytes of two tokens side by side: (a0, b0, a1, b1) and (a2, b2, a3, b3)
-#pragma unroll
-      for (int half = 0; half < 2; ++half) {
-        const uint32_t sel = half ? 0x7362 : 0x5140;
-        uint32_t x0, x1, y0, y1;
-        e4m3x4_f16(__byte_perm(cur.v[0][w], cur.v[1][w], sel), x0, x1);
-        e4m3x4_f16(__byte_perm(cur.v[2][w], cur.v[3][w], sel), y0, y1);
-        mma16816(o[4 * w + 2 * half], p0, p1, p2, p3, x0, y0);
-        mma16816(o[4 * w + 2 * half + 1], p0, p1, p2, p3, x1, y1);
-      }
-    }
+    __syncwarp();
+    if (lane == 0) mbar_arrive(&sm.empty[s]);
   }
 
-  // ---- the four warps' results joined
+  // ---- the four warps' results joined, over the ring (every copy has landed and been read)
+  named_bar_sync(1, kWarps * 32);
 #pragma unroll
   for (int x = 0; x < 2; ++x) {
     l[x] += __shfl_xor_sync(0xffffffffu, l[x], 1);
@@ -321,11 +413,12 @@ __global__ void __launch_bounds__(kWarps * 32, 2) cache_step_kernel(const CacheA
         y.w = fmaf(ow.w, ko, y.w);
       }
     }
-    const int qi = (r0 + r) / a.group, h = hk * a.group + (r0 + r) % a.group;
+    row_place(a, r0 + r, &qi, &qg);
+    const int h = hk * a.group + qg;
     if (sm.nan) {  // the row's own tokens of the zone: their NaN values reach its columns
       const int lr = key_limit(ex, a.causal, qi);
       float* yy = &y.x;
-      for (int u = max(c0 * kPage, lim_all / 16 * 16); u < min(lr, c1 * kPage); ++u) {
+      for (int u = max(c0 * kPage, lim_all / 32 * 32); u < min(lr, c1 * kPage); ++u) {
         const int page = page_of(a, b, u / kPage);
         if (page < 0) continue;
         const uint8_t* vr = a.v + page * a.page_stride + (static_cast<long long>(hk) * kPage + u % kPage) * D + cc;
@@ -350,17 +443,21 @@ __global__ void __launch_bounds__(kWarps * 32, 2) cache_step_kernel(const CacheA
 }
 
 // Joins the splits of one row: O and l brought to the largest reference. One
-// CTA per row, its four warps taking every fourth split; the order of the sums
-// is fixed.
+// CTA per row, each of its warps taking every so many-th split, eight of their
+// results in flight; the order of the sums is fixed.
+constexpr int kJoinWarps = 16;
+
 template <typename T, int D>
-__global__ void __launch_bounds__(128) cache_join_kernel(const CacheAttnArgs a) {
-  __shared__ float so[4][D];
-  __shared__ float sl[4];
-  const int tid = threadIdx.x, warp = tid / 32, lane = tid % 32;
+__global__ void __launch_bounds__(kJoinWarps * 32) cache_join_kernel(const CacheAttnArgs a) {
+  __shared__ float so[kJoinWarps][D];
+  __shared__ float sl[kJoinWarps];
+  const int tid = threadIdx.x, warp = tid / 32, lane = tid % 32, warps = blockDim.x / 32;
   const long long row = blockIdx.x;
   const int qi = static_cast<int>(row % a.N);
   const int h = static_cast<int>(row / a.N % a.H), b = static_cast<int>(row / a.N / a.H);
-  if (qi >= extent(a, b, false).cnt) return;
+  const int cnt = a.counts ? __ldg(a.counts + b) : a.N;
+  asm volatile("griddepcontrol.wait;" ::: "memory");  // the parts are there
+  if (qi >= cnt) return;
   const float2* ml = a.part_ml + row * a.splits;
   float mj = -INFINITY;
   for (int s = lane; s < a.splits; s += 32) mj = fmaxf(mj, ml[s].x);
@@ -370,57 +467,94 @@ __global__ void __launch_bounds__(128) cache_join_kernel(const CacheAttnArgs a) 
   float y[C], l = 0.f;
 #pragma unroll
   for (int e = 0; e < C; ++e) y[e] = 0.f;
-#pragma unroll 4
-  for (int s = warp; s < a.splits; s += 4) {
+#pragma unroll 8
+  for (int s = warp; s < a.splits; s += warps) {
     const float2 p = ml[s];
-    if (p.x == -INFINITY && p.y == 0.f) continue;  // saw nothing of the row
-    const float k = p.x == -INFINITY ? 1.f : ex2_approx(p.x - mj);
-    l = fmaf(p.y, k, l);
     const float* o = a.part_o + (row * a.splits + s) * D + lane * C;
+    float v[C];
+    if constexpr (C == 4) *reinterpret_cast<float4*>(v) = *reinterpret_cast<const float4*>(o);
+    else *reinterpret_cast<float2*>(v) = *reinterpret_cast<const float2*>(o);
+    const bool none = p.x == -INFINITY && p.y == 0.f;  // saw nothing of the row
+    const float k = p.x == -INFINITY ? 1.f : ex2_approx(p.x - mj);
+    l = none ? l : fmaf(p.y, k, l);
 #pragma unroll
-    for (int e = 0; e < C; ++e) y[e] = fmaf(o[e], k, y[e]);
+    for (int e = 0; e < C; ++e) y[e] = none ? y[e] : fmaf(v[e], k, y[e]);
   }
 #pragma unroll
   for (int e = 0; e < C; ++e) so[warp][lane * C + e] = y[e];
   if (lane == 0) sl[warp] = l;
   __syncthreads();
   if (tid < D / 2) {
-    const float lj = sl[0] + sl[1] + sl[2] + sl[3];
-    const float inv = lj != 0.f ? 1.f / lj : 0.f;
     const int c = 2 * tid;
-    const float y0 = so[0][c] + so[1][c] + so[2][c] + so[3][c];
-    const float y1 = so[0][c + 1] + so[1][c + 1] + so[2][c + 1] + so[3][c + 1];
+    float lj = 0.f, y0 = 0.f, y1 = 0.f;
+    for (int w = 0; w < warps; ++w) {
+      lj += sl[w];
+      y0 += so[w][c];
+      y1 += so[w][c + 1];
+    }
+    const float inv = lj != 0.f ? 1.f / lj : 0.f;
     uint16_t* dst = a.out + b * a.ost.b + h * a.ost.h + static_cast<long long>(qi) * a.ost.n + c;
     *reinterpret_cast<uint32_t*>(dst) = pack2<T>(y0 * inv, y1 * inv);
     if (tid == 0 && a.lse) a.lse[row] = lj == 0.f ? -INFINITY : (mj - kPBias + log2f(lj)) * kLn2C;
   }
 }
 
-template <typename T>
+// Keys or values of a cache as a 4D tensor {d, 64, heads, pages} of bytes; one
+// load brings a page of one head.
+bool page_map(CUtensorMap* map, const uint8_t* base, const CacheAttnArgs& a) {
+  EncodeTiledFn enc = get_encode_fn();
+  if (!enc) return false;
+  cuuint64_t dims[4] = {static_cast<cuuint64_t>(a.d), kPage, static_cast<cuuint64_t>(a.Hk),
+                        static_cast<cuuint64_t>(a.pages)};
+  cuuint64_t strides[3] = {static_cast<cuuint64_t>(a.d), static_cast<cuuint64_t>(kPage) * a.d,
+                           static_cast<cuuint64_t>(a.page_stride)};
+  cuuint32_t box[4] = {static_cast<cuuint32_t>(a.d), kPage, 1, 1};
+  cuuint32_t estr[4] = {1, 1, 1, 1};
+  return enc(map, CU_TENSOR_MAP_DATA_TYPE_UINT8, 4, const_cast<uint8_t*>(base), dims, strides, box, estr,
+             CU_TENSOR_MAP_INTERLEAVE_NONE, a.d == 128 ? CU_TENSOR_MAP_SWIZZLE_128B : CU_TENSOR_MAP_SWIZZLE_64B,
+             CU_TENSOR_MAP_L2_PROMOTION_L2_256B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
+}
+
+template <typename T, int D>
 cudaError_t launch_step_t(const CacheAttnArgs& a, cudaStream_t stream) {
+  CUtensorMap tmK, tmV;
+  if (!page_map(&tmK, a.k, a) || !page_map(&tmV, a.v, a)) return cudaErrorInvalidValue;
+  const size_t smem = sizeof(StepSmem<D>) + 1024;
+  const cudaError_t e = cudaFuncSetAttribute(cache_step_kernel<T, D>, cudaFuncAttributeMaxDynamicSharedMemorySize,
+                                             static_cast<int>(smem));
+  if (e != cudaSuccess) return e;
   const int tiles = (a.N * a.group + kRows - 1) / kRows;
-  const dim3 grid(a.splits, tiles * a.Hk, a.B);
-  if (a.d == 64) cache_step_kernel<T, 64><<<grid, kWarps * 32, 0, stream>>>(a);
-  else cache_step_kernel<T, 128><<<grid, kWarps * 32, 0, stream>>>(a);
+  cache_step_kernel<T, D><<<dim3(a.splits, tiles * a.Hk, a.B), (kWarps + 1) * 32, smem, stream>>>(tmK, tmV, a);
   return cudaGetLastError();
 }
 
-template <typename T>
+template <typename T, int D>
 cudaError_t launch_join_t(const CacheAttnArgs& a, cudaStream_t stream) {
-  const unsigned int rows = static_cast<unsigned int>(static_cast<long long>(a.B) * a.H * a.N);
-  if (a.d == 64) cache_join_kernel<T, 64><<<rows, 128, 0, stream>>>(a);
-  else cache_join_kernel<T, 128><<<rows, 128, 0, stream>>>(a);
-  return cudaGetLastError();
+  // set up while the parts are still computed (programmatic launch); a warp per
+  // four splits, D / 64 warps at least (the last step has D / 2 threads)
+  const int warps = a.splits <= 16 ? 4 : (a.splits <= 32 ? 8 : kJoinWarps);
+  cudaLaunchAttribute attr{};
+  attr.id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  attr.val.programmaticStreamSerializationAllowed = 1;
+  cudaLaunchConfig_t cfg{};
+  cfg.gridDim = dim3(static_cast<unsigned int>(static_cast<long long>(a.B) * a.H * a.N));
+  cfg.blockDim = dim3(warps * 32);
+  cfg.stream = stream;
+  cfg.attrs = &attr;
+  cfg.numAttrs = 1;
+  return cudaLaunchKernelEx(&cfg, cache_join_kernel<T, D>, a);
 }
 
 }  // namespace
 
 cudaError_t launch_cache_step(const CacheAttnArgs& a, cudaStream_t stream) {
-  return a.dtype == kF16 ? launch_step_t<__half>(a, stream) : launch_step_t<__nv_bfloat16>(a, stream);
+  if (a.dtype == kF16) return a.d == 64 ? launch_step_t<__half, 64>(a, stream) : launch_step_t<__half, 128>(a, stream);
+  return a.d == 64 ? launch_step_t<__nv_bfloat16, 64>(a, stream) : launch_step_t<__nv_bfloat16, 128>(a, stream);
 }
 
 cudaError_t launch_cache_join(const CacheAttnArgs& a, cudaStream_t stream) {
-  return a.dtype == kF16 ? launch_join_t<__half>(a, stream) : launch_join_t<__nv_bfloat16>(a, stream);
+  if (a.dtype == kF16) return a.d == 64 ? launch_join_t<__half, 64>(a, stream) : launch_join_t<__half, 128>(a, stream);
+  return a.d == 64 ? launch_join_t<__nv_bfloat16, 64>(a, stream) : launch_join_t<__nv_bfloat16, 128>(a, stream);
 }
 
 }  // namespace solattn

@@ -16,6 +16,7 @@
 
 #include "kernels.h"
 #include "ptx.cuh"
+#include "tensor_map.h"
 
 namespace solattn {
 namespace {
@@ -622,22 +623,6 @@ __device__ __forceinline__ uint32_t bias_pair(float w) {
 // ---------------------------------------------------------------------------
 // Host side: tensor maps and launch
 // ---------------------------------------------------------------------------
-using EncodeTiledFn = CUresult (*)(CUtensorMap*, CUtensorMapDataType, cuuint32_t, void*, const cuuint64_t*,
-                                   const cuuint64_t*, const cuuint32_t*, const cuuint32_t*, CUtensorMapInterleave,
-                                   CUtensorMapSwizzle, CUtensorMapL2promotion, CUtensorMapFloatOOBfill);
-
-EncodeTiledFn get_encode_fn() {
-  static EncodeTiledFn fn = nullptr;
-  if (!fn) {
-    void* p = nullptr;
-    cudaDriverEntryPointQueryResult q;
-    if (cudaGetDriverEntryPoint("cuTensorMapEncodeTiled", &p, cudaEnableDefault, &q) == cudaSuccess &&
-        q == cudaDriverEntryPointSuccess)
-      fn = reinterpret_cast<EncodeTiledFn>(p);
-  }
-  return fn;
-}
-
 // q, k or v as a 4D tensor {D, N, H, B} (D fastest) with the caller's element
 // strides; box = 64 columns x `rows` tokens of one (b, h), 128-byte swizzle;
 // tokens past N read as zero.

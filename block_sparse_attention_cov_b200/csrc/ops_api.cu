@@ -2,6 +2,7 @@
 // rotary positions, rotary positions with the pooled statistics, and the 8-bit
 // key/value cache. Argument checks and stream-ordered launches; no allocation.
 #include <cuda_runtime.h>
+#include <algorithm>
 #include <cmath>
 #include <cstdint>
 
@@ -341,12 +342,33 @@ namespace solattn {
 CachePlan cache_plan(int B, int H, int Hk, int N, int d, int columns) {
   constexpr int kSms = 148;
   const long long rows = static_cast<long long>(N) * (H / Hk);
-  CachePlan p{rows <= 64, 1};
+  // Rows of one key head in tiles of 16 that read the cache once each, or in tiles
+  // of 256 on tcgen05. 64 key heads of 16384 tokens: 32 rows 179 and 278 us, 48 rows
+  // 257 and 280 us, 64 rows 331 and 280 us.
+  CachePlan p{rows <= 48, 1};
   auto ceil_div = [](long long x, long long y) { return (x + y - 1) / y; };
   if (p.step) {
+    // Three CTAs per SM: a part costs about 5 us to start and finish and 0.75 us
+    // per page, all parts together what memory gives (5.9 TB/s, and the start of
+    // every wave but the first); among several sequences, which differ in length,
+    // some of a part is left at the end. Counts that fill one to eight waves are compared: 8 key heads of 65536 tokens
+    // take 33 us in 37 parts, 43 us in 74; 32 sequences of 32000 tokens take 388 us
+    // whole, 352 us in 3 parts; of 8000 to 32700 tokens 373 us, 231 us in 8.
     const long long units = static_cast<long long>(B) * Hk * ceil_div(rows, 16);
-    // three waves of two CTAs per SM, at least four pages a part
-    p.splits = static_cast<int>(std::fmax(1, std::fmin(ceil_div(6 * kSms, units), ceil_div(columns, 4))));
+    const double memory = static_cast<double>(units) * columns * 128 * d / 5.9e6;
+    double best = 0;
+    for (int w = 0; w <= 8; ++w) {
+      const long long s = w == 0 ? 1 : std::min<long long>(3ll * kSms * w / units, columns);
+      if (s < 1) continue;
+      const double join = s == 1 ? 0 : 2 + static_cast<double>(B) * H * N * s * d * 8 / 6e6;
+      const double part = 5 + 0.75 * ceil_div(columns, s);
+      const long long waves = ceil_div(units * s, 3 * kSms);
+      const double cost = std::max(waves * part, memory + 5 * (waves - 1)) + join + (B > 1 ? 0.15 * part : 0);
+      if (w == 0 || cost < best) {
+        best = cost;
+        p.splits = static_cast<int>(s);
+      }
+    }
   } else {
     // One CTA per SM: a part of the key axis costs about 9 us to start and finish
     // and 2.5 us per key tile (two pages), parts run in waves of 148, and what is
