@@ -10,8 +10,11 @@
 // count towards the scale.
 //
 // Bound by memory (2 or 4 bytes read and 1 written per element). One CTA per
-// page touched, head and tensor: the new rows stay in registers between the
-// maximum and the conversion, so they are read once.
+// page touched, head and tensor: the new rows stay in registers, as they were
+// read, between the maximum and the conversion. Their loads go out before the
+// page's number is looked up, and the maximum is taken on the bits (magnitudes of
+// 16-bit elements in pairs), so that what a thread holds is 16 bytes a row and
+// enough CTAs fit an SM to cover the latency.
 #include <cuda_bf16.h>
 #include <cuda_fp16.h>
 #include <cuda_runtime.h>
@@ -28,13 +31,23 @@ namespace {
 constexpr int kPage = 64;
 constexpr unsigned int kErrPage = 9;  // == SOLATTN_ERR_PAGE
 
-__device__ __forceinline__ void load8(const float* p, float (&f)[8]) {
-  const float4 a = *reinterpret_cast<const float4*>(p), b = *reinterpret_cast<const float4*>(p + 4);
-  f[0] = a.x; f[1] = a.y; f[2] = a.z; f[3] = a.w;
-  f[4] = b.x; f[5] = b.y; f[6] = b.z; f[7] = b.w;
-}
-__device__ __forceinline__ void load8(const __nv_bfloat16* p, float (&f)[8]) {
-  const uint4 w = *reinterpret_cast<const uint4*>(p);
+// Eight elements of a row as they lie in memory: their largest magnitude's bits,
+// and their values.
+template <typename T>
+struct Raw {  // 16-bit types
+  uint4 w;
+  __device__ __forceinline__ void load(const T* p) { w = __ldg(reinterpret_cast<const uint4*>(p)); }
+  __device__ __forceinline__ void zero() { w = make_uint4(0, 0, 0, 0); }
+  __device__ __forceinline__ uint32_t top() const {
+    const uint32_t m = __vmaxu2(__vmaxu2(w.x & 0x7fff7fffu, w.y & 0x7fff7fffu),
+                                __vmaxu2(w.z & 0x7fff7fffu, w.w & 0x7fff7fffu));
+    return max(m & 0xffffu, m >> 16);
+  }
+  __device__ __forceinline__ void get(float (&f)[8]) const;
+  static __device__ __forceinline__ float value(uint32_t bits);  // of a magnitude
+};
+template <>
+__device__ __forceinline__ void Raw<__nv_bfloat16>::get(float (&f)[8]) const {
   const uint32_t u[4] = {w.x, w.y, w.z, w.w};
 #pragma unroll
   for (int i = 0; i < 4; ++i) {
@@ -42,8 +55,10 @@ __device__ __forceinline__ void load8(const __nv_bfloat16* p, float (&f)[8]) {
     f[2 * i + 1] = __uint_as_float(u[i] & 0xffff0000u);
   }
 }
-__device__ __forceinline__ void load8(const __half* p, float (&f)[8]) {
-  const uint4 w = *reinterpret_cast<const uint4*>(p);
+template <>
+__device__ __forceinline__ float Raw<__nv_bfloat16>::value(uint32_t bits) { return __uint_as_float(bits << 16); }
+template <>
+__device__ __forceinline__ void Raw<__half>::get(float (&f)[8]) const {
   const uint32_t u[4] = {w.x, w.y, w.z, w.w};
 #pragma unroll
   for (int i = 0; i < 4; ++i) {
@@ -52,6 +67,29 @@ __device__ __forceinline__ void load8(const __half* p, float (&f)[8]) {
     f[2 * i + 1] = v.y;
   }
 }
+template <>
+__device__ __forceinline__ float Raw<__half>::value(uint32_t bits) {
+  return __half2float(__ushort_as_half(static_cast<unsigned short>(bits)));
+}
+template <>
+struct Raw<float> {
+  uint4 w, x;
+  __device__ __forceinline__ void load(const float* p) {
+    w = __ldg(reinterpret_cast<const uint4*>(p));
+    x = __ldg(reinterpret_cast<const uint4*>(p) + 1);
+  }
+  __device__ __forceinline__ void zero() { w = x = make_uint4(0, 0, 0, 0); }
+  __device__ __forceinline__ uint32_t top() const {
+    constexpr uint32_t M = 0x7fffffffu;
+    return max(max(max(w.x & M, w.y & M), max(w.z & M, w.w & M)), max(max(x.x & M, x.y & M), max(x.z & M, x.w & M)));
+  }
+  __device__ __forceinline__ void get(float (&f)[8]) const {
+    const uint32_t u[8] = {w.x, w.y, w.z, w.w, x.x, x.y, x.z, x.w};
+#pragma unroll
+    for (int i = 0; i < 8; ++i) f[i] = __uint_as_float(u[i]);
+  }
+  static __device__ __forceinline__ float value(uint32_t bits) { return __uint_as_float(bits); }
+};
 
 __device__ __forceinline__ uint32_t to_e4m3x2(float lo, float hi) {
   uint16_t r;
@@ -82,7 +120,7 @@ __device__ __forceinline__ float pow2i(int e) { return __int_as_float((127 + e) 
 template <typename T, int D>
 __global__ void __launch_bounds__(128) cache_append_kernel(const CacheAppendArgs a) {
   constexpr int CH = D / 8, RG = 128 / CH, RPT = kPage / RG;
-  __shared__ float wmax[4];
+  __shared__ uint32_t wmax[4];
   const int h = blockIdx.y, b = blockIdx.z >> 1, which = blockIdx.z & 1;
   const int tid = threadIdx.x, c = tid % CH, g = tid / CH;
   const long long cap = static_cast<long long>(a.columns) * kPage;
@@ -95,56 +133,61 @@ __global__ void __launch_bounds__(128) cache_append_kernel(const CacheAppendArgs
   }
   const int col = start / kPage + blockIdx.x;
   const int lo = max(start, col * kPage), hi = min(static_cast<long long>(start) + cnt, (col + 1ll) * kPage);
-  int page = -1;
-  if (lo < hi) {
-    page = __ldg(a.table + b * a.table_stride + col);
-    if (page < 0 || page >= a.pages) bad = true, page = -1;
+  if (lo >= hi) {
+    if (bad && tid == 0 && a.status && atomicCAS(&a.status->error, 0u, kErrPage) == 0u) a.status->unit = b;
+    return;
   }
-  if (bad && tid == 0 && a.status && atomicCAS(&a.status->error, 0u, kErrPage) == 0u) a.status->unit = b;
-  if (page < 0) return;
-
   const int first = lo - col * kPage, last = hi - col * kPage;  // rows of the page that are new
   const T* src = static_cast<const T*>(a.x[which]) + b * a.st.b + h * a.st.h + c * 8;
-  uint8_t* dst = a.data[which] + page * a.page_stride + static_cast<long long>(h) * kPage * D + c * 8;
-  float* sp = a.scale[which] + page * a.scale_stride + h;
-  const float old_scale = first > 0 ? *sp : 0.f;
-  float f[RPT][8];
-  float mx = 0.f;
+  int page = __ldg(a.table + b * a.table_stride + col);
+  Raw<T> x[RPT];
 #pragma unroll
   for (int r = 0; r < RPT; ++r) {
     const int row = g + r * RG;
-    if (row >= first && row < last) {
-      load8(src + static_cast<long long>(row + col * kPage - start) * a.st.n, f[r]);
-    } else {
-#pragma unroll
-      for (int e = 0; e < 8; ++e) f[r][e] = 0.f;
-    }
+    if (row >= first && row < last) x[r].load(src + static_cast<long long>(row + col * kPage - start) * a.st.n);
+    else x[r].zero();
   }
+  if (page < 0 || page >= a.pages) bad = true, page = -1;
+  if (bad && tid == 0 && a.status && atomicCAS(&a.status->error, 0u, kErrPage) == 0u) a.status->unit = b;
+  if (page < 0) return;
+  uint8_t* dst = a.data[which] + page * a.page_stride + static_cast<long long>(h) * kPage * D + c * 8;
+  float* sp = a.scale[which] + page * a.scale_stride + h;
+  const float old_scale = first > 0 ? *sp : 0.f;
+  uint32_t top = 0;
 #pragma unroll
-  for (int r = 0; r < RPT; ++r) {
-#pragma unroll
-    for (int e = 0; e < 8; ++e) {
-      const float m = fabsf(f[r][e]);
-      if (m < INFINITY) mx = fmaxf(mx, m);
-      else f[r][e] = NAN;
-    }
-  }
-#pragma unroll
-  for (int off = 16; off > 0; off >>= 1) mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, off));
-  if ((tid & 31) == 0) wmax[tid >> 5] = mx;
+  for (int r = 0; r < RPT; ++r) top = max(top, x[r].top());
+  top = __reduce_max_sync(0xffffffffu, top);
+  if ((tid & 31) == 0) wmax[tid >> 5] = top;
   __syncthreads();  // every thread has read the old scale too
-  mx = fmaxf(fmaxf(wmax[0], wmax[1]), fmaxf(wmax[2], wmax[3]));
-  const int e = scale_exponent(mx);
-  const float scale = fmaxf(pow2i(e), old_scale);
+  float mx = Raw<T>::value(max(max(wmax[0], wmax[1]), max(wmax[2], wmax[3])));
+  const bool finite = mx < INFINITY;
+  if (!finite) {  // rare: the largest finite magnitude, element by element
+    mx = 0.f;
+#pragma unroll
+    for (int r = 0; r < RPT; ++r) {
+      float f[8];
+      x[r].get(f);
+#pragma unroll
+      for (int e = 0; e < 8; ++e) mx = fabsf(f[e]) < INFINITY ? fmaxf(mx, fabsf(f[e])) : mx;
+    }
+    mx = __uint_as_float(__reduce_max_sync(0xffffffffu, __float_as_uint(mx)));
+    __syncthreads();  // the first maxima have been read
+    if ((tid & 31) == 0) wmax[tid >> 5] = __float_as_uint(mx);
+    __syncthreads();
+    mx = __uint_as_float(max(max(wmax[0], wmax[1]), max(wmax[2], wmax[3])));
+  }
+  const float scale = fmaxf(pow2i(scale_exponent(mx)), old_scale);
   const float inv = 1.f / scale;
   if (tid == 0) *sp = scale;
 #pragma unroll
   for (int r = 0; r < RPT; ++r) {
     const int row = g + r * RG;
     if (row >= first && row < last) {
+      float f[8];
+      x[r].get(f);
 #pragma unroll
-      for (int x = 0; x < 8; ++x) f[r][x] *= inv;
-      *reinterpret_cast<uint2*>(dst + row * D) = to_e4m3x8(f[r]);
+      for (int e = 0; e < 8; ++e) f[e] = finite || fabsf(f[e]) < INFINITY ? f[e] * inv : NAN;
+      *reinterpret_cast<uint2*>(dst + row * D) = to_e4m3x8(f);
     }
   }
   if (first > 0 && scale > old_scale) {  // the older tokens follow the page's new scale
