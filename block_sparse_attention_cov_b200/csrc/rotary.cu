@@ -270,7 +270,7 @@ cudaError_t launch_rotary_l(const RotaryArgs& a, int num_sms, cudaStream_t strea
 constexpr int kPoolBlock = 64;
 
 template <int D, int LAYOUT>
-__global__ void __launch_bounds__(256) rotary_pool_kernel(const RotaryPoolArgs a, int nb, int per_slice) {
+__global__ void __launch_bounds__(256, 2) rotary_pool_kernel(const RotaryPoolArgs a, int nb, int per_slice) {
   constexpr int U = D / 16;         // lanes per row
   constexpr int RPW = 32 / U;       // rows per warp and step
   constexpr int STEPS = kPoolBlock / RPW;
@@ -302,17 +302,25 @@ __global__ void __launch_bounds__(256) rotary_pool_kernel(const RotaryPoolArgs a
     float s0[8], s1[8];
 #pragma unroll
     for (int e = 0; e < 8; ++e) s0[e] = s1[e] = 0.f;
-    for (int st = 0; st < STEPS; st += UNROLL) {
-      uint4 w0[UNROLL], w1[UNROLL];
+    // four steps are multiplied while the next four are on their way
+    uint4 w0[UNROLL], w1[UNROLL], n0[UNROLL], n1[UNROLL];
+    auto load = [&](int st) {
 #pragma unroll
       for (int x = 0; x < UNROLL; ++x) {
         const int r = (st + x) * RPW + rl;
-        w0[x] = w1[x] = make_uint4(0, 0, 0, 0);
+        n0[x] = n1[x] = make_uint4(0, 0, 0, 0);
         if (r < rows) {
-          w0[x] = *reinterpret_cast<const uint4*>(src + r * a.st.n);
-          w1[x] = *reinterpret_cast<const uint4*>(src + r * a.st.n + D / 2);
+          n0[x] = *reinterpret_cast<const uint4*>(src + r * a.st.n);
+          n1[x] = *reinterpret_cast<const uint4*>(src + r * a.st.n + D / 2);
         }
       }
+    };
+    load(0);
+#pragma unroll 1
+    for (int st = 0; st < STEPS; st += UNROLL) {
+#pragma unroll
+      for (int x = 0; x < UNROLL; ++x) w0[x] = n0[x], w1[x] = n1[x];
+      if (st + UNROLL < STEPS) load(st + UNROLL);
 #pragma unroll
       for (int x = 0; x < UNROLL; ++x) {
         const int r = (st + x) * RPW + rl;
@@ -395,7 +403,9 @@ cudaError_t launch_rotary_pool_t(const RotaryPoolArgs& a, int num_sms, cudaStrea
   // over, fewer (each slice forms its own sines) where they do not
   const long long want = (4ll * num_sms * 4 + blocks - 1) / blocks;
   int per = static_cast<int>(want >= a.H ? 1 : (a.H + want - 1) / want);
-  if (per < 3 && a.H >= 3) per = 3;  // 9 items for 8 warps
+  // three items a head for eight warps: eight heads leave no warp over
+  if (a.H >= 8) per = (per + 7) / 8 * 8;
+  else if (per < 3 && a.H >= 3) per = 3;
   rotary_pool_kernel<D, LAYOUT><<<dim3(static_cast<unsigned int>(blocks), (a.H + per - 1) / per), 256, 0, stream>>>(
       a, nb, per);
   return cudaGetLastError();
