@@ -58,13 +58,14 @@ def _check_inputs(*ts):
     """q, k, v (and out): CUDA bf16 [B, H, N, d] with contiguous d and one common
     set of strides (contiguous, [B, N, H, d] seen through a permute, padded
     rows, ...)."""
+    shape, strides = ts[0].shape, ts[0].stride()
     for t in ts:
         if not (t.is_cuda and t.dtype == torch.bfloat16 and t.dim() == 4 and t.stride(-1) == 1):
             raise ValueError("q, k, v must be CUDA bf16 [B, H, N, d] tensors with contiguous d")
-    if not all(t.shape == ts[0].shape for t in ts):
-        raise ValueError("q, k, v must have the same shape")
-    if not all(t.stride() == ts[0].stride() for t in ts):
-        raise ValueError("q, k, v must share their strides")
+        if t.shape != shape:
+            raise ValueError("q, k, v must have the same shape")
+        if t.stride() != strides:
+            raise ValueError("q, k, v must share their strides")
 
 
 def _strides(t):
@@ -157,14 +158,23 @@ class PooledStats:
     shape: tuple
 
     def view(self, name: str) -> torch.Tensor:
-        B, H, N, d = self.shape
-        nb = (N + _lib.BLOCK - 1) // _lib.BLOCK
-        dims = (B, H, d) if name == "kmean" else (B, H, d, d) if name == "kcov" else (B, H, nb, d)
-        dt, size = (torch.bfloat16, 2) if name.endswith("16") else (torch.float32, 4)
-        off = getattr(self.struct, name) - self.buffer.data_ptr()
-        strides = (H * d, d, 1) if name == "kmean" else (H * dims[2] * d, dims[2] * d, d, 1)
-        whole = self.buffer.view(dt)
-        return whole.as_strided(dims, strides, whole.storage_offset() + off // size)
+        dtype, dims, strides, off = _pooled_view(self.shape, name)
+        whole = self.__dict__.get(dtype)
+        if whole is None:
+            whole = self.__dict__[dtype] = self.buffer.view(dtype)
+        return whole.as_strided(dims, strides, whole.storage_offset() + off)
+
+
+@functools.lru_cache(maxsize=512)
+def _pooled_view(shape, name: str):
+    """(type, dimensions, strides, offset in elements) of an array of the pooled statistics."""
+    B, H, N, d = shape
+    nb = (N + _lib.BLOCK - 1) // _lib.BLOCK
+    dims = (B, H, d) if name == "kmean" else (B, H, d, d) if name == "kcov" else (B, H, nb, d)
+    strides = (H * d, d, 1) if name == "kmean" else (H * dims[2] * d, dims[2] * d, d, 1)
+    dtype, size = (torch.bfloat16, 2) if name.endswith("16") else (torch.float32, 4)
+    offsets = dict(zip((n for n, _ in _lib.PooledStruct._fields_), _pooled_offsets(*shape)[1]))
+    return dtype, dims, strides, offsets[name] // size
 
 
 @functools.lru_cache(maxsize=512)
