@@ -12,12 +12,18 @@
 //                   TMEM (P in fp16 over the first half of its own S), O scaled
 //                   in TMEM only when a row's reference moves
 //   warps 8-11      cache pages to fp16 operands, four pages in shared memory
-//   warp 12         issues every MMA (warps 13-15 only give their registers)
+//   warp 12         issues every MMA
+//   warp 13         brings the cache's pages into shared memory, two pages ahead
+//                   of their conversion (loads into the converters' registers, a
+//                   page ahead, were waited for: 2,000 cycles under load)
+//   warps 14, 15    only give their registers
 //
-// Keys go in tiles of two pages: one QK of 128 columns (at 64 columns the QK of a
-// tile took as long: its A operand is read from shared memory either way), then
-// softmax and PV page by page, so that PV of the first page runs under the
-// softmax of the second.
+// Keys go in tiles of two pages, softmax and PV page by page, so that PV of the
+// first page runs under the softmax of the second. At d = 64 QK goes by pages too:
+// the next scores of a page's columns are there when the softmax comes back to
+// them. At d = 128 a QK of 64 columns takes as long as one of 128 (it is bound by
+// reading Q from shared memory; 520 cycles against 600), so there it is one QK of
+// 128 columns behind the tile's second PV, and the softmax waits for it.
 #include <cuda_runtime.h>
 #include <cmath>
 #include <cstdint>
@@ -33,10 +39,11 @@ constexpr int kChunkThreads = 512;  // 16 warps, 128 registers per thread at lau
 constexpr int kTileKeys = 2 * kPage;
 constexpr int kKStages = 2;  // key tiles
 constexpr int kVStages = 4;  // pages
+constexpr int kRaw = 2;      // pages as they lie in the cache
 constexpr int kInfo = 8;     // pages
 
 enum : uint32_t {
-  kSiteCQ = 40, kSiteCKFull, kSiteCKEmpty, kSiteCVFull, kSiteCVEmpty, kSiteCSFull, kSiteCPFull, kSiteCPv,
+  kSiteCQ = 40, kSiteCRawFull, kSiteCRawEmpty, kSiteCKFull, kSiteCKEmpty, kSiteCVFull, kSiteCVEmpty, kSiteCSFull, kSiteCPFull, kSiteCPv,
 };
 
 template <int D>
@@ -44,9 +51,11 @@ struct __align__(1024) ChunkSmem {
   uint8_t q[2][kTileRows * D * 2];        // SW128 K-major panels of 128 rows
   uint8_t k[kKStages][kTileKeys * D * 2]; // the same
   uint8_t v[kVStages][kPage * D * 2];     // SW128 panels of 64 rows
+  uint8_t raw[kRaw][2][kPage * D];        // keys and values of a page, e4m3
   float2 info[kInfo];                     // scales of a page's keys and values
   uint64_t q_full[2], k_full[kKStages], k_empty[kKStages], v_full[kVStages], v_empty[kVStages];
-  uint64_t s_full[2], p_full[2][2], pv_done[2][2], mma_done;
+  uint64_t raw_full[kRaw], raw_empty[kRaw];
+  uint64_t s_full[2][2], p_full[2][2], pv_done[2][2], mma_done;
   float row_inv[2][kTileRows];            // factor of each query row's scores
   uint32_t tmem_base;
   int abort_flag;
@@ -128,12 +137,12 @@ __device__ __forceinline__ float page_addend(const PageScale& ps, float m) {
 template <int D>
 static __device__ __noinline__ void scale_o(uint32_t taddr, float f) {
 #pragma unroll 1
-  for (int ch = 0; ch < D / 16; ++ch) {
-    uint32_t ov[16];
-    tmem_ld16_wait(taddr + ch * 16, ov);
+  for (int ch = 0; ch < D / 32; ++ch) {
+    uint32_t ov[32];
+    tmem_ld32_wait(taddr + ch * 32, ov);
 #pragma unroll
-    for (int x = 0; x < 16; ++x) ov[x] = __float_as_uint(__uint_as_float(ov[x]) * f);
-    tmem_st16_wait(taddr + ch * 16, ov);
+    for (int x = 0; x < 32; ++x) ov[x] = __float_as_uint(__uint_as_float(ov[x]) * f);
+    tmem_st32_wait(taddr + ch * 32, ov);
   }
 }
 
@@ -146,6 +155,14 @@ __device__ __forceinline__ bool chunk_wait(uint64_t* bar, uint32_t parity, volat
 
 // Byte offset of 16-byte chunk `ch` (8 fp16) of row `row` in a panel with 128-byte rows, 128-byte swizzle.
 __device__ __forceinline__ uint32_t sw128(int row, int ch) { return row * 128 + ((ch ^ (row & 7)) << 4); }
+
+// An untiled asynchronous copy of `bytes` from global to shared memory.
+__device__ __forceinline__ void bulk_load(void* dst, const void* src, uint32_t bytes, uint64_t* bar) {
+  asm volatile(
+      "cp.async.bulk.shared::cluster.global.mbarrier::complete_tx::bytes [%0], [%1], %2, [%3];" ::"r"(smem_u32(dst)),
+      "l"(src), "r"(bytes), "r"(smem_u32(bar))
+      : "memory");
+}
 
 __device__ __forceinline__ void st_shared_v4(void* p, uint32_t a, uint32_t b, uint32_t c, uint32_t d) {
   asm volatile("st.shared.v4.b32 [%0], {%1,%2,%3,%4};" ::"r"(smem_u32(p)), "r"(a), "r"(b), "r"(c), "r"(d) : "memory");
@@ -224,6 +241,7 @@ __device__ __forceinline__ void store_rows(const CacheAttnArgs& a, const uint8_t
 
 template <typename Elem, int D>
 __global__ void __launch_bounds__(kChunkThreads, 1) cache_chunk_kernel(const CacheAttnArgs a, int tiles) {
+  constexpr bool kPageSlots = D == 64;
   extern __shared__ uint8_t smem_raw[];
   ChunkSmem<D>& sm =
       *reinterpret_cast<ChunkSmem<D>*>(smem_raw + ((1024u - (smem_u32(smem_raw) & 1023u)) & 1023u));
@@ -244,13 +262,17 @@ __global__ void __launch_bounds__(kChunkThreads, 1) cache_chunk_kernel(const Cac
       mbar_init(&sm.v_empty[i], 1);
     }
     for (int i = 0; i < 2; ++i) {
-      mbar_init(&sm.s_full[i], 2);  // the MMAs' commit, and the issuer itself, which passes on the page scales
       for (int e = 0; e < 2; ++e) {
+        mbar_init(&sm.s_full[i][e], 2);  // the MMAs' commit, and the issuer itself, which passes on the page scales
         mbar_init(&sm.p_full[i][e], 4);
         mbar_init(&sm.pv_done[i][e], 1);
       }
     }
     for (int i = 0; i < 2; ++i) mbar_init(&sm.q_full[i], 4);
+    for (int i = 0; i < kRaw; ++i) {
+      mbar_init(&sm.raw_full[i], 1);
+      mbar_init(&sm.raw_empty[i], 4);
+    }
     mbar_init(&sm.mma_done, 1);
     sm.abort_flag = 0;
     sm.nan = 0;
@@ -283,66 +305,127 @@ __global__ void __launch_bounds__(kChunkThreads, 1) cache_chunk_kernel(const Cac
     tmem_relinquish();
     __syncwarp();
     const uint32_t tmem = *static_cast<volatile uint32_t*>(&sm.tmem_base);
-    constexpr uint32_t idesc_qk = idesc_f16_f32(kTileRows, kTileKeys, false);
+    constexpr uint32_t idesc_qk = idesc_f16_f32(kTileRows, kPageSlots ? kPage : kTileKeys, false);
     constexpr uint32_t idesc_pv = idesc_f16_f32(kTileRows, D, true);
     const uint64_t qd0 = sw128_desc(smem_u32(&sm.q[0][0]), 16, 1024);
     const uint64_t kd0 = sw128_desc(smem_u32(&sm.k[0][0]), 16, 1024);
     const uint64_t vd0 = sw128_desc(smem_u32(&sm.v[0][0]), 8192, 1024);
-    // QK of key tile t for tile x
-    auto qk = [&](int t, int x) {
-      tc_fence_after();
-      if (elect_one()) {
-        const uint64_t kd = kd0 + ((t % kKStages) * (kTileKeys * D * 2) >> 4);
+    // One thread issues everything and waits for what it needs; the others go on
+    // to the teardown.
+    if (elect_one()) {
+      auto wait = [&](uint64_t* bar, uint32_t parity, uint32_t site) {
+        return mbar_wait(bar, parity, abort_flag, st, site, blockIdx.x);
+      };
+      // QK for tile x: of key tile t = n (d = 128), of page n (d = 64)
+      auto qk = [&](int n, int x) {
+        tc_fence_after();
+        const int t = kPageSlots ? n / 2 : n, e = kPageSlots ? n & 1 : 0;
+        const uint64_t kd = kd0 + (((t % kKStages) * (kTileKeys * D * 2) + e * (kPage * 128)) >> 4);
         const uint64_t qd = qd0 + (x * (kTileRows * D * 2) >> 4);
 #pragma unroll
         for (int kk = 0; kk < D / 16; ++kk) {
           const uint32_t off = ((kk / 4) * (kTileRows * 128) + (kk % 4) * 32) >> 4;
-          mma_ss(tmem + x * 128, qd + off, kd + off, idesc_qk, kk > 0 ? 1u : 0u);
+          mma_ss(tmem + x * 128 + e * 64, qd + off, kd + off, idesc_qk, kk > 0 ? 1u : 0u);
         }
-        mbar_arrive(&sm.s_full[x]);
-        mma_commit(&sm.s_full[x]);
-        if (x == nq - 1) mma_commit(&sm.k_empty[t % kKStages]);
+        mbar_arrive(&sm.s_full[x][e]);
+        mma_commit(&sm.s_full[x][e]);
+        if (x == nq - 1 && (!kPageSlots || e == 1)) mma_commit(&sm.k_empty[t % kKStages]);
+      };
+      auto k_there = [&](int t) { return wait(&sm.k_full[t % kKStages], (t / kKStages) & 1, kSiteCKFull); };
+      bool ok = P == 0 || k_there(0);
+      for (int x = 0; x < nq && ok && P > 0; ++x) {
+        ok = wait(&sm.q_full[x], 0, kSiteCQ);
+        if (ok) qk(0, x);
+        if (ok && kPageSlots) qk(1, x);
       }
-      __syncwarp();
-    };
-    auto k_there = [&](int t) {
-      return chunk_wait(&sm.k_full[t % kKStages], (t / kKStages) & 1, abort_flag, st, kSiteCKFull, blockIdx.x);
-    };
-    const int T = P / 2;
-    bool ok = T == 0 || k_there(0);
-    for (int x = 0; x < nq && ok && T > 0; ++x) {
-      ok = chunk_wait(&sm.q_full[x], 0, abort_flag, st, kSiteCQ, blockIdx.x);
-      if (ok) qk(0, x);
-    }
-    for (int t = 0; t < T && ok; ++t) {
-      if (t + 1 < T) ok = k_there(t + 1);
-      for (int x = 0; x < nq && ok; ++x) {
-        for (int e = 0; e < 2 && ok; ++e) {
-          const int p = 2 * t + e;
-          if (x == 0) ok = chunk_wait(&sm.v_full[p % kVStages], (p / kVStages) & 1, abort_flag, st, kSiteCVFull, blockIdx.x);
-          if (ok) ok = chunk_wait(&sm.p_full[x][e], t & 1, abort_flag, st, kSiteCPFull, blockIdx.x);
-          if (!ok) break;
-          tc_fence_after();
-          if (elect_one()) {
-            const uint64_t vd = vd0 + ((p % kVStages) * (kPage * D * 2) >> 4);
+      // PV of page p for tile x
+      auto pv = [&](int p, int x) {
+        if (!wait(&sm.p_full[x][p & 1], (p >> 1) & 1, kSiteCPFull)) return false;
+        tc_fence_after();
+        const uint64_t vd = vd0 + ((p % kVStages) * (kPage * D * 2) >> 4);
 #pragma unroll
-            for (int kk = 0; kk < kPage / 16; ++kk)
-              mma_ts(tmem + 256 + x * 128, tmem + x * 128 + e * 64 + kk * 8, vd + ((kk * 2048) >> 4), idesc_pv,
-                     (p > 0 || kk > 0) ? 1u : 0u);
-            mma_commit(&sm.pv_done[x][e]);
-            if (x == nq - 1) mma_commit(&sm.v_empty[p % kVStages]);
+        for (int kk = 0; kk < kPage / 16; ++kk)
+          mma_ts(tmem + 256 + x * 128, tmem + x * 128 + (p & 1) * 64 + kk * 8, vd + ((kk * 2048) >> 4), idesc_pv,
+                 (p > 0 || kk > 0) ? 1u : 0u);
+        mma_commit(&sm.pv_done[x][p & 1]);
+        if (x == nq - 1) mma_commit(&sm.v_empty[p % kVStages]);
+        return true;
+      };
+      auto v_there = [&](int p) { return wait(&sm.v_full[p % kVStages], (p / kVStages) & 1, kSiteCVFull); };
+      // Scores go over the columns that a PV read P from, behind it: one thread's
+      // MMAs execute in order.
+      if constexpr (kPageSlots) {
+        for (int p = 0; p < P && ok; ++p) {
+          if ((p & 1) == 0 && p + 2 < P) ok = k_there(p / 2 + 1);
+          if (ok) ok = v_there(p);
+          for (int x = 0; x < nq && ok; ++x) {
+            ok = pv(p, x);
+            if (ok && p + 2 < P) qk(p + 2, x);
           }
-          __syncwarp();
         }
-        // the next key tile's scores, behind the PV that reads P from the same
-        // columns (one thread's MMAs execute in order)
-        if (ok && t + 1 < T) qk(t + 1, x);
+      } else {
+        for (int t = 0; t < P / 2 && ok; ++t) {
+          if (t + 1 < P / 2) ok = k_there(t + 1);
+          for (int x = 0; x < nq && ok; ++x) {
+            for (int e = 0; e < 2 && ok; ++e) {
+              if (x == 0) ok = v_there(2 * t + e);
+              if (ok) ok = pv(2 * t + e, x);
+            }
+            if (ok && t + 1 < P / 2) qk(t + 1, x);
+          }
+        }
       }
+      mma_commit(&sm.mma_done);  // teardown: issued MMAs complete before TMEM is freed
     }
-    if (elect_one()) mma_commit(&sm.mma_done);  // teardown: issued MMAs complete before TMEM is freed
     __syncwarp();
     mbar_wait_quiet(&sm.mma_done, 0);
     __syncwarp();
+    } else if (warp == 13) {
+      // ======================= pages on their way =======================
+      const int32_t* table = a.table + b * a.table_stride + c0;
+      bool ok = true;
+      int issued = 0;
+      for (int base = 0; base < P && ok; base += 32) {
+        // 32 pages' numbers and scales at once; -1 and 0: not there
+        int pg = -1;
+        float ks = 0.f, vs = 0.f;
+        if (base + lane < pend) {
+          pg = __ldg(table + base + lane);
+          if (pg < 0 || pg >= a.pages) {
+            report_page(st, b);
+            pg = -1;
+          } else {
+            ks = __ldg(a.k_scale + pg * a.scale_stride + hk);
+            vs = __ldg(a.v_scale + pg * a.scale_stride + hk);
+          }
+        }
+        for (int i = 0; i < min(32, P - base) && ok; ++i) {
+          const int p = base + i, s = p % kRaw;
+          const int page = __shfl_sync(0xffffffffu, pg, i);
+          const float2 kv = make_float2(__shfl_sync(0xffffffffu, ks, i), __shfl_sync(0xffffffffu, vs, i));
+          if (p >= kRaw)
+            ok = chunk_wait(&sm.raw_empty[s], ((p / kRaw) & 1) ^ 1, abort_flag, st, kSiteCRawEmpty, blockIdx.x);
+          if (ok && lane == 0) {
+            // the scales' slot held page p - 8: page p - 2 has been converted, so the QK of page p - 6 is
+            // complete, and it was issued behind P of page p - 8 in both tiles
+            sm.info[p % kInfo] = kv;
+            if (page >= 0) {
+              const long long at = page * a.page_stride + static_cast<long long>(hk) * kPage * D;
+              mbar_arrive_expect_tx(&sm.raw_full[s], 2 * kPage * D);
+              bulk_load(sm.raw[s][0], a.k + at, kPage * D, &sm.raw_full[s]);
+              bulk_load(sm.raw[s][1], a.v + at, kPage * D, &sm.raw_full[s]);
+            } else {
+              mbar_arrive(&sm.raw_full[s]);
+            }
+            issued = p + 1;
+          }
+          __syncwarp();
+        }
+      }
+      // teardown: every copy has landed (none is under way unless a wait gave up)
+      if (lane == 0)
+        for (int p = max(0, issued - kRaw); p < issued; ++p) mbar_wait_quiet(&sm.raw_full[p % kRaw], (p / kRaw) & 1);
+      __syncwarp();
     }
   } else if (warp >= 8) {
     regs_dec<104>();
@@ -354,26 +437,11 @@ __global__ void __launch_bounds__(kChunkThreads, 1) cache_chunk_kernel(const Cac
     // chunk of the row and row of the pass: eight neighbouring lanes take four chunks of two rows
     const int c = LPR == 4 ? ct % 4 : ct % 4 + 4 * (ct / 8 % 2);
     const int rr = LPR == 4 ? ct / 4 : ct / 4 % 2 + 2 * (ct / 16);
-    const long long lane_off = static_cast<long long>(hk) * kPage * D + rr * D + 16 * c;
-    const int32_t* table = a.table + b * a.table_stride + c0;
-    // the table's entry for step p (-1: no such step), and what is made of it when it is used
-    auto entry = [&](int p) { return p < pend ? __ldg(table + p) : -1; };
-    auto checked = [&](int pg, int p) {
-      if (pg >= 0 && pg < a.pages) return pg;
-      if (p < pend) report_page(st, b);
-      return -1;
-    };
-    auto load = [&](uint4 (&w)[PASSES], const uint8_t* src, int pg, int row_end) {
-#pragma unroll
-      for (int i = 0; i < PASSES; ++i)
-        w[i] = (pg >= 0 && i * ROWS + rr < row_end)
-                   ? __ldg(reinterpret_cast<const uint4*>(src + pg * a.page_stride + lane_off + i * ROWS * D))
-                   : make_uint4(0, 0, 0, 0);
-    };
     // 16 e4m3 of a row become two 16-byte chunks of fp16. A quarter-warp's eight
     // stores cover two rows' chunks of one panel: eight different bank groups.
     const int ch = 2 * (c % 4);
     const uint32_t off0 = sw128(rr, ch), off1 = sw128(rr, ch + 1);  // ROWS is a multiple of the swizzle's 8 rows
+    const int at = rr * D + 16 * c;  // of the thread's 16 bytes in a page, and every ROWS rows on
     auto store = [&](const uint4 (&w)[PASSES], uint8_t* dst, int panel_rows) {
       uint8_t* base = dst + (c / 4) * (panel_rows * 128);
 #pragma unroll
@@ -387,65 +455,47 @@ __global__ void __launch_bounds__(kChunkThreads, 1) cache_chunk_kernel(const Cac
         st_shared_v4(base + off1 + i * ROWS * 128, f[4], f[5], f[6], f[7]);
       }
     };
-    // Two pages of loads in flight in registers (a page takes about the time of
-    // one round trip to memory), their numbers a further two pages ahead.
-    uint4 kw[2][PASSES], vw[2][PASSES];
-    float ks[2], vs[2];
-    int next[2];
-    auto fetch_scale = [&](int e, int pg) {
-      ks[e] = vs[e] = 0.f;
-      if (ct == 0 && pg >= 0) {
-        ks[e] = __ldg(a.k_scale + pg * a.scale_stride + hk);
-        vs[e] = __ldg(a.v_scale + pg * a.scale_stride + hk);
-      }
-    };
-    auto fetch_v = [&](int e, int pg, int p) {  // rows behind the sequence as zeros: they may hold NaN
-      load(vw[e], a.v, pg, ex.len - (c0 + p) * kPage);
-    };
-#pragma unroll
-    for (int e = 0; e < 2; ++e) {
-      const int pg = checked(entry(e), e);
-      next[e] = entry(2 + e);
-      load(kw[e], a.k, pg, kPage);
-      fetch_v(e, pg, e);
-      fetch_scale(e, pg);
-    }
     bool ok = true;
-    for (int t = 0; t < P / 2 && ok; ++t) {
-      const int kst = t % kKStages;
-      if (t >= kKStages)
-        ok = chunk_wait(&sm.k_empty[kst], ((t / kKStages) & 1) ^ 1, abort_flag, st, kSiteCKEmpty, blockIdx.x);
+#pragma unroll 1
+    for (int p = 0; p < P && ok; ++p) {
+      const int kst = p / 2 % kKStages, vst = p % kVStages, rs = p % kRaw;
+      if ((p & 1) == 0 && p >= 2 * kKStages)
+        ok = chunk_wait(&sm.k_empty[kst], ((p / (2 * kKStages)) & 1) ^ 1, abort_flag, st, kSiteCKEmpty, blockIdx.x);
+      if (ok) ok = chunk_wait(&sm.raw_full[rs], (p / kRaw) & 1, abort_flag, st, kSiteCRawFull, blockIdx.x);
+      if (!ok) break;
+      uint4 w[PASSES];
 #pragma unroll
-      for (int e = 0; e < 2; ++e) {
-        const int p = 2 * t + e, vst = p % kVStages;
-        const int pg = checked(next[e], p + 2);
-        next[e] = entry(p + 4);
-        // the scales' slot held page p - 8, past in both tiles: the QK of pages p - 4 was issued behind P(p - 5)
-        if (ct == 0) sm.info[p % kInfo] = make_float2(ks[e], vs[e]);
-        store(kw[e], sm.k[kst] + e * kPage * 128, kTileKeys);
-        fence_proxy_async_smem();
-        __syncwarp();
-        if (lane == 0) mbar_arrive(&sm.k_full[kst]);
-        load(kw[e], a.k, pg, kPage);
-        fetch_scale(e, pg);
-        if (a.causal && (c0 + p + 1) * kPage > least) {  // a NaN value must reach only the rows that see its token
-          bool bad = false;
+      for (int i = 0; i < PASSES; ++i) w[i] = *reinterpret_cast<const uint4*>(sm.raw[rs][0] + at + i * ROWS * D);
+      store(w, sm.k[kst] + (p & 1) * kPage * 128, kTileKeys);
 #pragma unroll
-          for (int i = 0; i < PASSES; ++i) {
-            uint4& w = vw[e][i];
-            bad |= has_nan8(w.x) | has_nan8(w.y) | has_nan8(w.z) | has_nan8(w.w);
-            w = make_uint4(drop_nan8(w.x), drop_nan8(w.y), drop_nan8(w.z), drop_nan8(w.w));
-          }
-          if (bad) sm.nan = 1;
-        }
-        if (ok && p >= kVStages)
-          ok = chunk_wait(&sm.v_empty[vst], ((p / kVStages) & 1) ^ 1, abort_flag, st, kSiteCVEmpty, blockIdx.x);
-        store(vw[e], sm.v[vst], kPage);
-        fence_proxy_async_smem();
-        __syncwarp();
-        if (lane == 0) mbar_arrive(&sm.v_full[vst]);
-        fetch_v(e, pg, p + 2);
+      for (int i = 0; i < PASSES; ++i) w[i] = *reinterpret_cast<const uint4*>(sm.raw[rs][1] + at + i * ROWS * D);
+      const int rows_in = sm.info[p % kInfo].y == 0.f ? 0 : ex.len - (c0 + p) * kPage;
+      fence_proxy_async_smem();
+      __syncwarp();
+      if (lane == 0) {
+        mbar_arrive(&sm.k_full[kst]);
+        mbar_arrive(&sm.raw_empty[rs]);
       }
+      if (rows_in < kPage) {  // rows behind the sequence may hold anything, NaN too
+#pragma unroll
+        for (int i = 0; i < PASSES; ++i)
+          if (i * ROWS + rr >= rows_in) w[i] = make_uint4(0, 0, 0, 0);
+      }
+      if (a.causal && (c0 + p + 1) * kPage > least) {  // a NaN value must reach only the rows that see its token
+        bool bad = false;
+#pragma unroll
+        for (int i = 0; i < PASSES; ++i) {
+          bad |= has_nan8(w[i].x) | has_nan8(w[i].y) | has_nan8(w[i].z) | has_nan8(w[i].w);
+          w[i] = make_uint4(drop_nan8(w[i].x), drop_nan8(w[i].y), drop_nan8(w[i].z), drop_nan8(w[i].w));
+        }
+        if (bad) sm.nan = 1;
+      }
+      if (p >= kVStages)
+        ok = chunk_wait(&sm.v_empty[vst], ((p / kVStages) & 1) ^ 1, abort_flag, st, kSiteCVEmpty, blockIdx.x);
+      store(w, sm.v[vst], kPage);
+      fence_proxy_async_smem();
+      __syncwarp();
+      if (lane == 0) mbar_arrive(&sm.v_full[vst]);
     }
   } else {
     regs_inc<152>();
@@ -468,8 +518,8 @@ __global__ void __launch_bounds__(kChunkThreads, 1) cache_chunk_kernel(const Cac
     bool ok = true;
     const int lim_warp = __reduce_min_sync(0xffffffffu, lim);
     for (int p = 0; p < P; ++p) {
-      if ((p & 1) == 0) {
-        ok = chunk_wait<1>(&sm.s_full[x], (p >> 1) & 1, abort_flag, st, kSiteCSFull, blockIdx.x);
+      if (kPageSlots || (p & 1) == 0) {
+        ok = chunk_wait<1>(&sm.s_full[x][kPageSlots ? p & 1 : 0], (p >> 1) & 1, abort_flag, st, kSiteCSFull, blockIdx.x);
         if (!ok) break;
         tc_fence_after();
         if (p == 0) {
@@ -484,10 +534,11 @@ __global__ void __launch_bounds__(kChunkThreads, 1) cache_chunk_kernel(const Cac
       uint32_t sv[64], pw[32];
       tmem_ld32x2_wait(col, col + 32, sv);
       const int key0 = (c0 + p) * kPage;
-      if (key0 + kPage > lim_warp) {
+      if (key0 + kPage > lim_warp || kv.y == 0.f) {  // kv.y = 0: a page that is not there
+        const int end = kv.y == 0.f ? key0 : lim;
 #pragma unroll
         for (int i = 0; i < 64; ++i)
-          if (key0 + i >= lim) sv[i] = 0xff800000u;
+          if (key0 + i >= end) sv[i] = 0xff800000u;
       }
       const float c = row_scale(ps, rf);
       // P with the reference as it stands, beside the maximum rather than behind
@@ -497,7 +548,7 @@ __global__ void __launch_bounds__(kChunkThreads, 1) cache_chunk_kernel(const Cac
       while (true) {
         sum = page_weights(sv, c, page_addend(ps, m), pw);
         const float mx = page_max(sv);
-        const float tm = mx == -INFINITY || ps.vinv == 0.f ? -INFINITY : fmaf(mx, c, ps.ev);
+        const float tm = mx == -INFINITY ? -INFINITY : fmaf(mx, c, ps.ev);
         if (!__any_sync(0xffffffffu, tm > m + kSlack)) break;
         const float up = tm > m + kSlack ? ceilf(tm) : m;
         const float k = up == m || m == -INFINITY ? 1.f : ex2_approx(m - up);

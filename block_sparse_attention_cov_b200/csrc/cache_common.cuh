@@ -15,8 +15,8 @@
 // 1 / vs on the page's sum.
 //
 // P is rounded to fp16 for the value product (11 bits against bf16's 8, and
-// e4m3 is exact in fp16); 2^kPBias lifts the range so that weights 2^-31 below
-// the row's largest are still held, and the lazy reference (raised only when a
+// e4m3 is exact in fp16); 2^kPBias lifts the range so that weights 2^-29 of the
+// row's largest are still held, and the lazy reference (raised only when a
 // row's maximum passes it by kSlack) keeps P at 2^15 at most. Queries are scaled
 // by a power of two per row before they are rounded to fp16: exact for fp16
 // inputs, and for bf16 inputs down to 2^-23 of the row's largest element.
@@ -34,8 +34,8 @@ namespace solattn {
 namespace {
 
 constexpr int kPage = 64;
-constexpr float kPBias = 7.f;
-constexpr float kSlack = 8.f;
+constexpr float kPBias = 5.f;
+constexpr float kSlack = 10.f;
 constexpr float kLog2eC = 1.4426950408889634f;
 constexpr float kLn2C = 0.6931471805599453f;
 constexpr unsigned int kErrPage = 9;  // == SOLATTN_ERR_PAGE
