@@ -365,13 +365,15 @@ __global__ void __launch_bounds__(kChunkThreads, 1) cache_chunk_kernel(const Cac
         }
       } else {
         for (int t = 0; t < P / 2 && ok; ++t) {
-          if (t + 1 < P / 2) ok = k_there(t + 1);
           for (int x = 0; x < nq && ok; ++x) {
             for (int e = 0; e < 2 && ok; ++e) {
               if (x == 0) ok = v_there(2 * t + e);
               if (ok) ok = pv(2 * t + e, x);
             }
-            if (ok && t + 1 < P / 2) qk(t + 1, x);
+            if (ok && t + 1 < P / 2) {
+              if (x == 0) ok = k_there(t + 1);
+              if (ok) qk(t + 1, x);
+            }
           }
         }
       }
