@@ -56,7 +56,6 @@ struct __align__(1024) ChunkSmem {
   uint64_t q_full[2], k_full[kKStages], k_empty[kKStages], v_full[kVStages], v_empty[kVStages];
   uint64_t raw_full[kRaw], raw_empty[kRaw];
   uint64_t s_full[2][2], p_full[2][2], pv_done[2][2], mma_done;
-  float row_inv[2][kTileRows];            // factor of each query row's scores
   uint32_t tmem_base;
   int abort_flag;
   int nan;
@@ -103,23 +102,51 @@ __device__ __forceinline__ float page_max(const uint32_t (&sv)[64]) {
       t[e] = max3(t[e], __uint_as_float(sv[i + 2 * e]), __uint_as_float(sv[i + 2 * e + 1]));
   return fmaxf(max3(t[0], t[1], t[2]), t[3]);
 }
-// P = 2^(s c + add) of the page as 32 fp16 pairs; returns the sum.
+// 2^x of a pair on the FMA pipe: x = j + f with an integer j and |f| <= 1/2, a
+// polynomial of degree 4 (least squares, reweighted towards the least largest
+// relative error: 2.6e-6) for 2^f, times 2^j. -inf gives 2^-126, NaN stays NaN.
+__device__ __forceinline__ uint64_t f2_exp2(uint64_t v) {
+  float x0, x1;
+  f2_get(v, x0, x1);
+  asm("max.NaN.f32 %0, %0, %1;" : "+f"(x0) : "f"(-126.f));
+  asm("max.NaN.f32 %0, %0, %1;" : "+f"(x1) : "f"(-126.f));
+  const uint64_t x = f2_make(__float_as_uint(x0), __float_as_uint(x1));
+  const uint64_t t = f2_add(x, f2_both(12582912.f));   // 1.5 2^23: the low bits are j
+  const uint64_t f = f2_fma(f2_add(t, f2_both(-12582912.f)), f2_both(-1.f), x);
+  uint64_t p = f2_fma(f, f2_both(0.009570101276040077f), f2_both(0.05591786280274391f));
+  p = f2_fma(p, f, f2_both(0.240247443318367f));
+  p = f2_fma(p, f, f2_both(0.6931217908859253f));
+  p = f2_fma(p, f, f2_both(0.9999992847442627f));
+  float t0, t1;
+  f2_get(t, t0, t1);
+  const uint64_t scale = f2_make((__float_as_uint(t0) << 23) + 0x3f800000u, (__float_as_uint(t1) << 23) + 0x3f800000u);
+  uint64_t r;
+  asm("mul.rn.f32x2 %0, %1, %2;" : "=l"(r) : "l"(p), "l"(scale));
+  return r;
+}
+
+// P = 2^(s c + add) of the page as 32 fp16 pairs; returns the sum. Every
+// kPolyEvery-th pair goes to the FMA pipe.
+template <int kPolyEvery>
 __device__ __forceinline__ float page_weights(const uint32_t (&sv)[64], float c, float add, uint32_t* pw) {
   const uint64_t c2 = f2_both(c), a2 = f2_both(add);
   uint64_t l0 = 0, l1 = 0;
 #pragma unroll
-  for (int i = 0; i < 32; i += 2) {
-    float x0, x1, y0, y1;
-    f2_get(f2_fma(f2_make(sv[2 * i], sv[2 * i + 1]), c2, a2), x0, x1);
-    f2_get(f2_fma(f2_make(sv[2 * i + 2], sv[2 * i + 3]), c2, a2), y0, y1);
-    x0 = ex2_approx(x0);
-    x1 = ex2_approx(x1);
-    y0 = ex2_approx(y0);
-    y1 = ex2_approx(y1);
-    l0 = f2_add(l0, f2_make(__float_as_uint(x0), __float_as_uint(x1)));
-    l1 = f2_add(l1, f2_make(__float_as_uint(y0), __float_as_uint(y1)));
+  for (int i = 0; i < 32; ++i) {
+    uint64_t x = f2_fma(f2_make(sv[2 * i], sv[2 * i + 1]), c2, a2);
+    float x0, x1;
+    if (kPolyEvery > 0 && i % (kPolyEvery > 0 ? kPolyEvery : 1) == kPolyEvery - 1) {
+      x = f2_exp2(x);
+      f2_get(x, x0, x1);
+    } else {
+      f2_get(x, x0, x1);
+      x0 = ex2_approx(x0);
+      x1 = ex2_approx(x1);
+      x = f2_make(__float_as_uint(x0), __float_as_uint(x1));
+    }
+    if (i & 1) l1 = f2_add(l1, x);
+    else l0 = f2_add(l0, x);
     pw[i] = pack_f16x2(x0, x1);
-    pw[i + 1] = pack_f16x2(y0, y1);
   }
   float u, v;
   f2_get(f2_add(l0, l1), u, v);
@@ -170,47 +197,50 @@ __device__ __forceinline__ void st_shared_v4(void* p, uint32_t a, uint32_t b, ui
 
 // 32 rows of queries into the operand layout, scaled to fp16's range by a power
 // of two per row: copied as they are (a row's lanes side by side, so that a copy
-// touches a few lines and not one per lane), then converted in place.
+// touches a few lines and not one per lane), then every lane converts one row in
+// place. Returns the factor of the lane's row. The loops are short on purpose:
+// they run once, and what is unrolled is first fetched.
 template <typename Elem, int D>
-__device__ __forceinline__ void load_queries(const CacheAttnArgs& a, uint8_t* tile, float* row_inv, int b, int hk,
-                                             int first, int rows, int wq, int lane) {
+__device__ __forceinline__ float load_queries(const CacheAttnArgs& a, uint8_t* tile, int b, int hk, int first, int rows,
+                                              int wq, int lane) {
   constexpr int LPR = D / 8, RPL = 32 / LPR;  // lanes per row, rows per step
   const int ch = lane % LPR;
-  uint8_t* at = tile + (ch / 8) * (kTileRows * 128);
-#pragma unroll 2
+  uint8_t* to = tile + (ch / 8) * (kTileRows * 128);
+  const uint16_t* from = a.q + b * a.st.b + hk * a.group * a.st.h + 8 * ch;
+#pragma unroll 4
   for (int i = 0; i < 32 / RPL; ++i) {
     const int lr = wq * 32 + i * RPL + lane / LPR, r = first + lr;
     int qi, g;
     row_place(a, r, &qi, &g);
-    const uint16_t* src = a.q + b * a.st.b + (hk * a.group + g) * a.st.h + static_cast<long long>(qi) * a.st.n + 8 * ch;
-    asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(smem_u32(at + sw128(lr, ch % 8))),
-                 "l"(r < rows ? src : a.q), "r"(r < rows ? 16 : 0)
+    asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(smem_u32(to + sw128(lr, ch % 8))),
+                 "l"(r < rows ? from + g * a.st.h + qi * a.st.n : a.q), "r"(r < rows ? 16 : 0)
                  : "memory");
   }
   asm volatile("cp.async.wait_all;" ::: "memory");
+  __syncwarp();
+  const int lr = wq * 32 + lane;
+  uint8_t* row = tile + lr * 128;
+  const uint32_t x = static_cast<uint32_t>(lr & 7) << 4;
+  uint32_t top = 0;
 #pragma unroll 4
-  for (int i = 0; i < 32 / RPL; ++i) {  // every lane reads back what it copied
-    const int lr = wq * 32 + i * RPL + lane / LPR;
-    uint4* p = reinterpret_cast<uint4*>(at + sw128(lr, ch % 8));
+  for (int c = 0; c < D / 8; ++c) {  // largest magnitude's bits, by pairs
+    const uint4 w = *reinterpret_cast<const uint4*>(row + (c / 8) * (kTileRows * 128) + ((c % 8 * 16) ^ x));
+    constexpr uint32_t M = 0x7fff7fffu;
+    top = __vmaxu2(top, __vmaxu2(__vmaxu2(w.x & M, w.y & M), __vmaxu2(w.z & M, w.w & M)));
+  }
+  float mul, inv;
+  row_factor(unpack2<Elem>(max(top & 0xffffu, top >> 16)).x, &mul, &inv);
+#pragma unroll 2
+  for (int c = 0; c < D / 8; ++c) {
+    uint4* p = reinterpret_cast<uint4*>(row + (c / 8) * (kTileRows * 128) + ((c % 8 * 16) ^ x));
     const uint4 w = *p;
-    const uint32_t u[4] = {w.x, w.y, w.z, w.w};
-    float2 f[4];
-    float amax = 0.f;
-#pragma unroll
-    for (int e = 0; e < 4; ++e) {
-      f[e] = unpack2<Elem>(u[e]);
-      amax = fmaxf(amax, fmaxf(fabsf(f[e].x), fabsf(f[e].y)));
-    }
-#pragma unroll
-    for (int off = LPR / 2; off > 0; off >>= 1) amax = fmaxf(amax, __shfl_xor_sync(0xffffffffu, amax, off));
-    float mul, inv;
-    row_factor(amax, &mul, &inv);
-    *p = make_uint4(pack_f16x2(f[0].x * mul, f[0].y * mul), pack_f16x2(f[1].x * mul, f[1].y * mul),
-                    pack_f16x2(f[2].x * mul, f[2].y * mul), pack_f16x2(f[3].x * mul, f[3].y * mul));
-    if (ch == 0) row_inv[lr] = inv;
+    const float2 f0 = unpack2<Elem>(w.x), f1 = unpack2<Elem>(w.y), f2 = unpack2<Elem>(w.z), f3 = unpack2<Elem>(w.w);
+    *p = make_uint4(pack_f16x2(f0.x * mul, f0.y * mul), pack_f16x2(f1.x * mul, f1.y * mul),
+                    pack_f16x2(f2.x * mul, f2.y * mul), pack_f16x2(f3.x * mul, f3.y * mul));
   }
   fence_proxy_async_smem();
   __syncwarp();
+  return inv;
 }
 
 // A warp's 32 rows of D / 2 columns (half 0 or 1 of the row; columns of 4 bytes
@@ -242,6 +272,10 @@ __device__ __forceinline__ void store_rows(const CacheAttnArgs& a, const uint8_t
 template <typename Elem, int D>
 __global__ void __launch_bounds__(kChunkThreads, 1) cache_chunk_kernel(const CacheAttnArgs a, int tiles) {
   constexpr bool kPageSlots = D == 64;
+  // At d = 64 both tiles' exponentials always meet: every eighth pair on the FMA
+  // pipe instead takes 256 x 8192 x 148 heads from 136 to 127 us (every fourth: 135
+  // us). At d = 128 they alternate, and the longer code costs (151 to 159 us).
+  constexpr int kPolyEvery = D == 64 ? 8 : 0;
   extern __shared__ uint8_t smem_raw[];
   ChunkSmem<D>& sm =
       *reinterpret_cast<ChunkSmem<D>*>(smem_raw + ((1024u - (smem_u32(smem_raw) & 1023u)) & 1023u));
@@ -512,9 +546,8 @@ __global__ void __launch_bounds__(kChunkThreads, 1) cache_chunk_kernel(const Cac
     const int h = hk * a.group + g;
     const int lim = there ? key_limit(ex, a.causal, qi) : seen;  // a row that is not there masks nothing by itself
     const uint32_t lane_sel = static_cast<uint32_t>(wq * 32) << 16;
-    load_queries<Elem, D>(a, sm.q[x], sm.row_inv[x], b, hk, r0 + x * kTileRows, rows, wq, lane);
+    const float rf = load_queries<Elem, D>(a, sm.q[x], b, hk, r0 + x * kTileRows, rows, wq, lane);
     if (lane == 0) mbar_arrive(&sm.q_full[x]);
-    const float rf = sm.row_inv[x][lr];
     uint32_t colS = 0, colO = 0;
     float m = -INFINITY, l = 0.f;
     bool ok = true;
@@ -548,7 +581,7 @@ __global__ void __launch_bounds__(kChunkThreads, 1) cache_chunk_kernel(const Cac
       // ones) is done again
       float sum;
       while (true) {
-        sum = page_weights(sv, c, page_addend(ps, m), pw);
+        sum = page_weights<kPolyEvery>(sv, c, page_addend(ps, m), pw);
         const float mx = page_max(sv);
         const float tm = mx == -INFINITY ? -INFINITY : fmaf(mx, c, ps.ev);
         if (!__any_sync(0xffffffffu, tm > m + kSlack)) break;
