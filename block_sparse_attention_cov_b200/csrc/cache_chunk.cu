@@ -42,8 +42,18 @@ constexpr int kVStages = 4;  // pages
 constexpr int kRaw = 2;      // pages as they lie in the cache
 constexpr int kInfo = 8;     // pages
 
+// Wait sites reported in the status word.
 enum : uint32_t {
-  kSiteCQ = 40, kSiteCRawFull, kSiteCRawEmpty, kSiteCKFull, kSiteCKEmpty, kSiteCVFull, kSiteCVEmpty, kSiteCSFull, kSiteCPFull, kSiteCPv,
+  kSiteCQ = 40,
+  kSiteCRawFull,
+  kSiteCRawEmpty,
+  kSiteCKFull,
+  kSiteCKEmpty,
+  kSiteCVFull,
+  kSiteCVEmpty,
+  kSiteCSFull,
+  kSiteCPFull,
+  kSiteCPv,
 };
 
 template <int D>
@@ -104,12 +114,12 @@ __device__ __forceinline__ float page_max(const uint32_t (&sv)[64]) {
 }
 // 2^x of a pair on the FMA pipe: x = j + f with an integer j and |f| <= 1/2, a
 // polynomial of degree 4 (least squares, reweighted towards the least largest
-// relative error: 2.6e-6) for 2^f, times 2^j. -inf gives 2^-126, NaN stays NaN.
+// relative error: 2.6e-6) for 2^f, times 2^j (0 for j = -127). NaN stays NaN.
 __device__ __forceinline__ uint64_t f2_exp2(uint64_t v) {
   float x0, x1;
   f2_get(v, x0, x1);
-  asm("max.NaN.f32 %0, %0, %1;" : "+f"(x0) : "f"(-126.f));
-  asm("max.NaN.f32 %0, %0, %1;" : "+f"(x1) : "f"(-126.f));
+  asm("max.NaN.f32 %0, %0, %1;" : "+f"(x0) : "f"(-127.f));
+  asm("max.NaN.f32 %0, %0, %1;" : "+f"(x1) : "f"(-127.f));
   const uint64_t x = f2_make(__float_as_uint(x0), __float_as_uint(x1));
   const uint64_t t = f2_add(x, f2_both(12582912.f));   // 1.5 2^23: the low bits are j
   const uint64_t f = f2_fma(f2_add(t, f2_both(-12582912.f)), f2_both(-1.f), x);
@@ -334,88 +344,88 @@ __global__ void __launch_bounds__(kChunkThreads, 1) cache_chunk_kernel(const Cac
   if (warp >= 12) {
     regs_dec<104>();
     if (warp == 12) {
-    // ======================= MMA issuer =======================
-    tmem_alloc(&sm.tmem_base, 512);  // the softmax warps learn of it with the first scores
-    tmem_relinquish();
-    __syncwarp();
-    const uint32_t tmem = *static_cast<volatile uint32_t*>(&sm.tmem_base);
-    constexpr uint32_t idesc_qk = idesc_f16_f32(kTileRows, kPageSlots ? kPage : kTileKeys, false);
-    constexpr uint32_t idesc_pv = idesc_f16_f32(kTileRows, D, true);
-    const uint64_t qd0 = sw128_desc(smem_u32(&sm.q[0][0]), 16, 1024);
-    const uint64_t kd0 = sw128_desc(smem_u32(&sm.k[0][0]), 16, 1024);
-    const uint64_t vd0 = sw128_desc(smem_u32(&sm.v[0][0]), 8192, 1024);
-    // One thread issues everything and waits for what it needs; the others go on
-    // to the teardown.
-    if (elect_one()) {
-      auto wait = [&](uint64_t* bar, uint32_t parity, uint32_t site) {
-        return mbar_wait(bar, parity, abort_flag, st, site, blockIdx.x);
-      };
-      // QK for tile x: of key tile t = n (d = 128), of page n (d = 64)
-      auto qk = [&](int n, int x) {
-        tc_fence_after();
-        const int t = kPageSlots ? n / 2 : n, e = kPageSlots ? n & 1 : 0;
-        const uint64_t kd = kd0 + (((t % kKStages) * (kTileKeys * D * 2) + e * (kPage * 128)) >> 4);
-        const uint64_t qd = qd0 + (x * (kTileRows * D * 2) >> 4);
+      // ======================= MMA issuer =======================
+      tmem_alloc(&sm.tmem_base, 512);  // the softmax warps learn of it with the first scores
+      tmem_relinquish();
+      __syncwarp();
+      const uint32_t tmem = *static_cast<volatile uint32_t*>(&sm.tmem_base);
+      constexpr uint32_t idesc_qk = idesc_f16_f32(kTileRows, kPageSlots ? kPage : kTileKeys, false);
+      constexpr uint32_t idesc_pv = idesc_f16_f32(kTileRows, D, true);
+      const uint64_t qd0 = sw128_desc(smem_u32(&sm.q[0][0]), 16, 1024);
+      const uint64_t kd0 = sw128_desc(smem_u32(&sm.k[0][0]), 16, 1024);
+      const uint64_t vd0 = sw128_desc(smem_u32(&sm.v[0][0]), 8192, 1024);
+      // One thread issues everything and waits for what it needs; the others go on
+      // to the teardown.
+      if (elect_one()) {
+        auto wait = [&](uint64_t* bar, uint32_t parity, uint32_t site) {
+          return mbar_wait(bar, parity, abort_flag, st, site, blockIdx.x);
+        };
+        // QK for tile x: of key tile t = n (d = 128), of page n (d = 64)
+        auto qk = [&](int n, int x) {
+          tc_fence_after();
+          const int t = kPageSlots ? n / 2 : n, e = kPageSlots ? n & 1 : 0;
+          const uint64_t kd = kd0 + (((t % kKStages) * (kTileKeys * D * 2) + e * (kPage * 128)) >> 4);
+          const uint64_t qd = qd0 + (x * (kTileRows * D * 2) >> 4);
 #pragma unroll
-        for (int kk = 0; kk < D / 16; ++kk) {
-          const uint32_t off = ((kk / 4) * (kTileRows * 128) + (kk % 4) * 32) >> 4;
-          mma_ss(tmem + x * 128 + e * 64, qd + off, kd + off, idesc_qk, kk > 0 ? 1u : 0u);
-        }
-        mbar_arrive(&sm.s_full[x][e]);
-        mma_commit(&sm.s_full[x][e]);
-        if (x == nq - 1 && (!kPageSlots || e == 1)) mma_commit(&sm.k_empty[t % kKStages]);
-      };
-      auto k_there = [&](int t) { return wait(&sm.k_full[t % kKStages], (t / kKStages) & 1, kSiteCKFull); };
-      bool ok = P == 0 || k_there(0);
-      for (int x = 0; x < nq && ok && P > 0; ++x) {
-        ok = wait(&sm.q_full[x], 0, kSiteCQ);
-        if (ok) qk(0, x);
-        if (ok && kPageSlots) qk(1, x);
-      }
-      // PV of page p for tile x
-      auto pv = [&](int p, int x) {
-        if (!wait(&sm.p_full[x][p & 1], (p >> 1) & 1, kSiteCPFull)) return false;
-        tc_fence_after();
-        const uint64_t vd = vd0 + ((p % kVStages) * (kPage * D * 2) >> 4);
-#pragma unroll
-        for (int kk = 0; kk < kPage / 16; ++kk)
-          mma_ts(tmem + 256 + x * 128, tmem + x * 128 + (p & 1) * 64 + kk * 8, vd + ((kk * 2048) >> 4), idesc_pv,
-                 (p > 0 || kk > 0) ? 1u : 0u);
-        mma_commit(&sm.pv_done[x][p & 1]);
-        if (x == nq - 1) mma_commit(&sm.v_empty[p % kVStages]);
-        return true;
-      };
-      auto v_there = [&](int p) { return wait(&sm.v_full[p % kVStages], (p / kVStages) & 1, kSiteCVFull); };
-      // Scores go over the columns that a PV read P from, behind it: one thread's
-      // MMAs execute in order.
-      if constexpr (kPageSlots) {
-        for (int p = 0; p < P && ok; ++p) {
-          if ((p & 1) == 0 && p + 2 < P) ok = k_there(p / 2 + 1);
-          if (ok) ok = v_there(p);
-          for (int x = 0; x < nq && ok; ++x) {
-            ok = pv(p, x);
-            if (ok && p + 2 < P) qk(p + 2, x);
+          for (int kk = 0; kk < D / 16; ++kk) {
+            const uint32_t off = ((kk / 4) * (kTileRows * 128) + (kk % 4) * 32) >> 4;
+            mma_ss(tmem + x * 128 + e * 64, qd + off, kd + off, idesc_qk, kk > 0 ? 1u : 0u);
           }
+          mbar_arrive(&sm.s_full[x][e]);
+          mma_commit(&sm.s_full[x][e]);
+          if (x == nq - 1 && (!kPageSlots || e == 1)) mma_commit(&sm.k_empty[t % kKStages]);
+        };
+        auto k_there = [&](int t) { return wait(&sm.k_full[t % kKStages], (t / kKStages) & 1, kSiteCKFull); };
+        bool ok = P == 0 || k_there(0);
+        for (int x = 0; x < nq && ok && P > 0; ++x) {
+          ok = wait(&sm.q_full[x], 0, kSiteCQ);
+          if (ok) qk(0, x);
+          if (ok && kPageSlots) qk(1, x);
         }
-      } else {
-        for (int t = 0; t < P / 2 && ok; ++t) {
-          for (int x = 0; x < nq && ok; ++x) {
-            for (int e = 0; e < 2 && ok; ++e) {
-              if (x == 0) ok = v_there(2 * t + e);
-              if (ok) ok = pv(2 * t + e, x);
-            }
-            if (ok && t + 1 < P / 2) {
-              if (x == 0) ok = k_there(t + 1);
-              if (ok) qk(t + 1, x);
+        // PV of page p for tile x
+        auto pv = [&](int p, int x) {
+          if (!wait(&sm.p_full[x][p & 1], (p >> 1) & 1, kSiteCPFull)) return false;
+          tc_fence_after();
+          const uint64_t vd = vd0 + ((p % kVStages) * (kPage * D * 2) >> 4);
+#pragma unroll
+          for (int kk = 0; kk < kPage / 16; ++kk)
+            mma_ts(tmem + 256 + x * 128, tmem + x * 128 + (p & 1) * 64 + kk * 8, vd + ((kk * 2048) >> 4), idesc_pv,
+                   (p > 0 || kk > 0) ? 1u : 0u);
+          mma_commit(&sm.pv_done[x][p & 1]);
+          if (x == nq - 1) mma_commit(&sm.v_empty[p % kVStages]);
+          return true;
+        };
+        auto v_there = [&](int p) { return wait(&sm.v_full[p % kVStages], (p / kVStages) & 1, kSiteCVFull); };
+        // Scores go over the columns that a PV read P from, behind it: one thread's
+        // MMAs execute in order.
+        if constexpr (kPageSlots) {
+          for (int p = 0; p < P && ok; ++p) {
+            if ((p & 1) == 0 && p + 2 < P) ok = k_there(p / 2 + 1);
+            if (ok) ok = v_there(p);
+            for (int x = 0; x < nq && ok; ++x) {
+              ok = pv(p, x);
+              if (ok && p + 2 < P) qk(p + 2, x);
             }
           }
+        } else {
+          for (int t = 0; t < P / 2 && ok; ++t) {
+            for (int x = 0; x < nq && ok; ++x) {
+              for (int e = 0; e < 2 && ok; ++e) {
+                if (x == 0) ok = v_there(2 * t + e);
+                if (ok) ok = pv(2 * t + e, x);
+              }
+              if (ok && t + 1 < P / 2) {
+                if (x == 0) ok = k_there(t + 1);
+                if (ok) qk(t + 1, x);
+              }
+            }
+          }
         }
+        mma_commit(&sm.mma_done);  // teardown: issued MMAs complete before TMEM is freed
       }
-      mma_commit(&sm.mma_done);  // teardown: issued MMAs complete before TMEM is freed
-    }
-    __syncwarp();
-    mbar_wait_quiet(&sm.mma_done, 0);
-    __syncwarp();
+      __syncwarp();
+      mbar_wait_quiet(&sm.mma_done, 0);
+      __syncwarp();
     } else if (warp == 13) {
       // ======================= pages on their way =======================
       const int32_t* table = a.table + b * a.table_stride + c0;
@@ -536,135 +546,135 @@ __global__ void __launch_bounds__(kChunkThreads, 1) cache_chunk_kernel(const Cac
   } else {
     regs_inc<152>();
     if (warp / 4 < nq) {
-    // ======================= softmax =======================
-    const int x = warp / 4, wq = warp % 4;
-    const int lr = wq * 32 + lane;  // row of the tile == TMEM lane
-    const int r = r0 + x * kTileRows + lr;
-    const bool there = r < rows;
-    int qi, g;
-    row_place(a, r, &qi, &g);
-    const int h = hk * a.group + g;
-    const int lim = there ? key_limit(ex, a.causal, qi) : seen;  // a row that is not there masks nothing by itself
-    const uint32_t lane_sel = static_cast<uint32_t>(wq * 32) << 16;
-    const float rf = load_queries<Elem, D>(a, sm.q[x], b, hk, r0 + x * kTileRows, rows, wq, lane);
-    if (lane == 0) mbar_arrive(&sm.q_full[x]);
-    uint32_t colS = 0, colO = 0;
-    float m = -INFINITY, l = 0.f;
-    bool ok = true;
-    const int lim_warp = __reduce_min_sync(0xffffffffu, lim);
-    for (int p = 0; p < P; ++p) {
-      if (kPageSlots || (p & 1) == 0) {
-        ok = chunk_wait<1>(&sm.s_full[x][kPageSlots ? p & 1 : 0], (p >> 1) & 1, abort_flag, st, kSiteCSFull, blockIdx.x);
-        if (!ok) break;
-        tc_fence_after();
-        if (p == 0) {
-          const uint32_t tmem = *static_cast<volatile uint32_t*>(&sm.tmem_base);
-          colS = tmem + x * 128 + lane_sel;
-          colO = tmem + 256 + x * 128 + lane_sel;
-        }
-      }
-      const float2 kv = sm.info[p % kInfo];
-      const PageScale ps = page_scale(a, kv.x, kv.y);
-      const uint32_t col = colS + (p & 1) * 64;
-      uint32_t sv[64], pw[32];
-      tmem_ld32x2_wait(col, col + 32, sv);
-      const int key0 = (c0 + p) * kPage;
-      if (key0 + kPage > lim_warp || kv.y == 0.f) {  // kv.y = 0: a page that is not there
-        const int end = kv.y == 0.f ? key0 : lim;
-#pragma unroll
-        for (int i = 0; i < 64; ++i)
-          if (key0 + i >= end) sv[i] = 0xff800000u;
-      }
-      const float c = row_scale(ps, rf);
-      // P with the reference as it stands, beside the maximum rather than behind
-      // it; only a page that passes the reference by kSlack (rare after the first
-      // ones) is done again
-      float sum;
-      while (true) {
-        sum = page_weights<kPolyEvery>(sv, c, page_addend(ps, m), pw);
-        const float mx = page_max(sv);
-        const float tm = mx == -INFINITY ? -INFINITY : fmaf(mx, c, ps.ev);
-        if (!__any_sync(0xffffffffu, tm > m + kSlack)) break;
-        const float up = tm > m + kSlack ? ceilf(tm) : m;
-        const float k = up == m || m == -INFINITY ? 1.f : ex2_approx(m - up);
-        if (p > 0) {  // O follows, once the PV of the page before is complete
-          ok = chunk_wait<1>(&sm.pv_done[x][(p - 1) & 1], ((p - 1) >> 1) & 1, abort_flag, st, kSiteCPv, blockIdx.x);
+      // ======================= softmax =======================
+      const int x = warp / 4, wq = warp % 4;
+      const int lr = wq * 32 + lane;  // row of the tile == TMEM lane
+      const int r = r0 + x * kTileRows + lr;
+      const bool there = r < rows;
+      int qi, g;
+      row_place(a, r, &qi, &g);
+      const int h = hk * a.group + g;
+      const int lim = there ? key_limit(ex, a.causal, qi) : seen;  // a row that is not there masks nothing by itself
+      const uint32_t lane_sel = static_cast<uint32_t>(wq * 32) << 16;
+      const float rf = load_queries<Elem, D>(a, sm.q[x], b, hk, r0 + x * kTileRows, rows, wq, lane);
+      if (lane == 0) mbar_arrive(&sm.q_full[x]);
+      uint32_t colS = 0, colO = 0;
+      float m = -INFINITY, l = 0.f;
+      bool ok = true;
+      const int lim_warp = __reduce_min_sync(0xffffffffu, lim);
+      for (int p = 0; p < P; ++p) {
+        if (kPageSlots || (p & 1) == 0) {
+          ok = chunk_wait<1>(&sm.s_full[x][kPageSlots ? p & 1 : 0], (p >> 1) & 1, abort_flag, st, kSiteCSFull, blockIdx.x);
           if (!ok) break;
           tc_fence_after();
-          scale_o<D>(colO, k);
-        }
-        l *= k;
-        m = up;
-      }
-      if (!ok) break;
-      l = fmaf(sum, ps.vinv, l);
-      tmem_st32_wait(col, pw);
-      tc_fence_before();
-      __syncwarp();
-      if (lane == 0) mbar_arrive(&sm.p_full[x][p & 1]);
-    }
-    if (ok && P > 0) {
-      ok = chunk_wait<1>(&sm.pv_done[x][(P - 1) & 1], ((P - 1) >> 1) & 1, abort_flag, st, kSiteCPv, blockIdx.x);
-      tc_fence_after();
-    }
-    if (ok) {
-      // ---- the row's result, or its part. A warp's 32 rows go through its
-      // quarter of the Q tile (its last QK is complete) 64 columns at a time, so
-      // that the stores run along rows, a few lines each.
-      const bool part = a.splits > 1;
-      const float inv = part ? 1.f : (l != 0.f ? 1.f / l : 0.f);
-      const long long pr = partial_row(a, b, h, qi, split);
-      uint16_t* dst = a.out + b * a.ost.b + h * a.ost.h + static_cast<long long>(qi) * a.ost.n;
-      uint8_t* stage = sm.q[x] + wq * 32 * D * 2;  // 8 KB (D = 128) or 4 KB
-      constexpr int COLS = D / 2;                  // columns per pass: 32 rows of COLS floats, or D of 16 bits
-#pragma unroll 1
-      for (int half = 0; half < 2; ++half) {
-        uint32_t o[COLS];
-        if (P > 0) {
-          if constexpr (D == 128) tmem_ld32x2_wait(colO + half * 64, colO + half * 64 + 32, o);
-          else tmem_ld32_wait(colO + half * 32, o);
-        } else {
-#pragma unroll
-          for (int e = 0; e < COLS; ++e) o[e] = 0;
-        }
-        if (part) {
-#pragma unroll
-          for (int e = 0; e < COLS / 4; ++e)
-            st_shared_v4(stage + (lane * (COLS / 4) + ((e + lane) % (COLS / 4))) * 16, o[4 * e], o[4 * e + 1], o[4 * e + 2],
-                         o[4 * e + 3]);
-        } else {
-#pragma unroll
-          for (int e = 0; e < COLS / 8; ++e) {
-            uint32_t pk[4];
-#pragma unroll
-            for (int z = 0; z < 4; ++z)
-              pk[z] = pack2<Elem>(__uint_as_float(o[8 * e + 2 * z]) * inv, __uint_as_float(o[8 * e + 2 * z + 1]) * inv);
-            st_shared_v4(stage + (lane * (COLS / 8) + ((e + lane) % (COLS / 8))) * 16, pk[0], pk[1], pk[2], pk[3]);
+          if (p == 0) {
+            const uint32_t tmem = *static_cast<volatile uint32_t*>(&sm.tmem_base);
+            colS = tmem + x * 128 + lane_sel;
+            colO = tmem + 256 + x * 128 + lane_sel;
           }
         }
+        const float2 kv = sm.info[p % kInfo];
+        const PageScale ps = page_scale(a, kv.x, kv.y);
+        const uint32_t col = colS + (p & 1) * 64;
+        uint32_t sv[64], pw[32];
+        tmem_ld32x2_wait(col, col + 32, sv);
+        const int key0 = (c0 + p) * kPage;
+        if (key0 + kPage > lim_warp || kv.y == 0.f) {  // kv.y = 0: a page that is not there
+          const int end = kv.y == 0.f ? key0 : lim;
+#pragma unroll
+          for (int i = 0; i < 64; ++i)
+            if (key0 + i >= end) sv[i] = 0xff800000u;
+        }
+        const float c = row_scale(ps, rf);
+        // P with the reference as it stands, beside the maximum rather than behind
+        // it; only a page that passes the reference by kSlack (rare after the first
+        // ones) is done again
+        float sum;
+        while (true) {
+          sum = page_weights<kPolyEvery>(sv, c, page_addend(ps, m), pw);
+          const float mx = page_max(sv);
+          const float tm = mx == -INFINITY ? -INFINITY : fmaf(mx, c, ps.ev);
+          if (!__any_sync(0xffffffffu, tm > m + kSlack)) break;
+          const float up = tm > m + kSlack ? ceilf(tm) : m;
+          const float k = up == m || m == -INFINITY ? 1.f : ex2_approx(m - up);
+          if (p > 0) {  // O follows, once the PV of the page before is complete
+            ok = chunk_wait<1>(&sm.pv_done[x][(p - 1) & 1], ((p - 1) >> 1) & 1, abort_flag, st, kSiteCPv, blockIdx.x);
+            if (!ok) break;
+            tc_fence_after();
+            scale_o<D>(colO, k);
+          }
+          l *= k;
+          m = up;
+        }
+        if (!ok) break;
+        l = fmaf(sum, ps.vinv, l);
+        tmem_st32_wait(col, pw);
+        tc_fence_before();
         __syncwarp();
-        if (part) store_rows<COLS / 4>(a, stage, b, hk, r - lane, rows, half, split, lane);
-        else store_rows<COLS / 8>(a, stage, b, hk, r - lane, rows, half, split, lane);
+        if (lane == 0) mbar_arrive(&sm.p_full[x][p & 1]);
       }
-      if (there) {
-        if (part) a.part_ml[pr] = make_float2(m, l);
-        else if (a.lse)
-          a.lse[(static_cast<long long>(b) * a.H + h) * a.N + qi] =
-              l == 0.f ? -INFINITY : (m - kPBias + log2f(l)) * kLn2C;
+      if (ok && P > 0) {
+        ok = chunk_wait<1>(&sm.pv_done[x][(P - 1) & 1], ((P - 1) >> 1) & 1, abort_flag, st, kSiteCPv, blockIdx.x);
+        tc_fence_after();
       }
-      if (there && sm.nan) {  // NaN values among the tokens that only some rows see
-        for (int u = max(c0 * kPage, least / kPage * kPage); u < min(lim, (c0 + pend) * kPage); ++u) {
-          const int page = page_of(a, b, u / kPage);
-          if (page < 0) continue;
-          const uint8_t* vr = a.v + page * a.page_stride + (static_cast<long long>(hk) * kPage + u % kPage) * D;
-          for (int e = 0; e < D; ++e) {
-            if ((vr[e] & 0x7f) != 0x7f) continue;
-            if (part) a.part_o[pr * D + e] = NAN;
-            else dst[e] = static_cast<uint16_t>(pack2<Elem>(NAN, NAN) & 0xffffu);
+      if (ok) {
+        // ---- the row's result, or its part. A warp's 32 rows go through its
+        // quarter of the Q tile (its last QK is complete) 64 columns at a time, so
+        // that the stores run along rows, a few lines each.
+        const bool part = a.splits > 1;
+        const float inv = part ? 1.f : (l != 0.f ? 1.f / l : 0.f);
+        const long long pr = partial_row(a, b, h, qi, split);
+        uint16_t* dst = a.out + b * a.ost.b + h * a.ost.h + static_cast<long long>(qi) * a.ost.n;
+        uint8_t* stage = sm.q[x] + wq * 32 * D * 2;  // 8 KB (D = 128) or 4 KB
+        constexpr int COLS = D / 2;                  // columns per pass: 32 rows of COLS floats, or D of 16 bits
+#pragma unroll 1
+        for (int half = 0; half < 2; ++half) {
+          uint32_t o[COLS];
+          if (P > 0) {
+            if constexpr (D == 128) tmem_ld32x2_wait(colO + half * 64, colO + half * 64 + 32, o);
+            else tmem_ld32_wait(colO + half * 32, o);
+          } else {
+#pragma unroll
+            for (int e = 0; e < COLS; ++e) o[e] = 0;
+          }
+          if (part) {
+#pragma unroll
+            for (int e = 0; e < COLS / 4; ++e)
+              st_shared_v4(stage + (lane * (COLS / 4) + ((e + lane) % (COLS / 4))) * 16, o[4 * e], o[4 * e + 1], o[4 * e + 2],
+                           o[4 * e + 3]);
+          } else {
+#pragma unroll
+            for (int e = 0; e < COLS / 8; ++e) {
+              uint32_t pk[4];
+#pragma unroll
+              for (int z = 0; z < 4; ++z)
+                pk[z] = pack2<Elem>(__uint_as_float(o[8 * e + 2 * z]) * inv, __uint_as_float(o[8 * e + 2 * z + 1]) * inv);
+              st_shared_v4(stage + (lane * (COLS / 8) + ((e + lane) % (COLS / 8))) * 16, pk[0], pk[1], pk[2], pk[3]);
+            }
+          }
+          __syncwarp();
+          if (part) store_rows<COLS / 4>(a, stage, b, hk, r - lane, rows, half, split, lane);
+          else store_rows<COLS / 8>(a, stage, b, hk, r - lane, rows, half, split, lane);
+        }
+        if (there) {
+          if (part) a.part_ml[pr] = make_float2(m, l);
+          else if (a.lse)
+            a.lse[(static_cast<long long>(b) * a.H + h) * a.N + qi] =
+                l == 0.f ? -INFINITY : (m - kPBias + log2f(l)) * kLn2C;
+        }
+        if (there && sm.nan) {  // NaN values among the tokens that only some rows see
+          for (int u = max(c0 * kPage, least / kPage * kPage); u < min(lim, (c0 + pend) * kPage); ++u) {
+            const int page = page_of(a, b, u / kPage);
+            if (page < 0) continue;
+            const uint8_t* vr = a.v + page * a.page_stride + (static_cast<long long>(hk) * kPage + u % kPage) * D;
+            for (int e = 0; e < D; ++e) {
+              if ((vr[e] & 0x7f) != 0x7f) continue;
+              if (part) a.part_o[pr * D + e] = NAN;
+              else dst[e] = static_cast<uint16_t>(pack2<Elem>(NAN, NAN) & 0xffffu);
+            }
           }
         }
       }
-    }
     }
   }
 

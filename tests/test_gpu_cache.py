@@ -195,6 +195,21 @@ def test_attention_of_zero_queries_and_zero_values():
         assert torch.allclose(lse, torch.full_like(lse, math.log(150)), atol=2.0 ** -15)
 
 
+@pytest.mark.parametrize("d", [64, 128])
+@pytest.mark.parametrize("exponent", [-32, 0, 6, 32])
+def test_rows_that_see_nothing_at_any_value_scale(d, exponent):
+    """200 queries of a sequence of 50 tokens: the first 150 rows give 0 and -inf, whatever the pages' scales; the others
+    are finite."""
+    c = sa.Cache.empty(1, 1, d)
+    c.k.view(torch.uint8).random_(0, 0x70, generator=torch.Generator("cuda").manual_seed(1))
+    c.v.view(torch.uint8).random_(0, 0x70, generator=torch.Generator("cuda").manual_seed(2))
+    c.k_scale.fill_(0.01), c.v_scale.fill_(2.0 ** exponent)
+    q = torch.randn((1, 2, 200, d), generator=_gen(14)).to(torch.bfloat16).cuda()
+    out, lse = _attend(q, c, torch.zeros((1, 1), dtype=torch.int32), [50], None, True)
+    assert (out[:, :, :150] == 0).all() and (lse[:, :, :150] == -math.inf).all()
+    assert torch.isfinite(out).all() and torch.isfinite(lse[:, :, 150:]).all() and (out[:, :, 150:] != 0).any(-1).all()
+
+
 @pytest.mark.parametrize("N", [3, 40, 150])
 def test_attention_not_finite(N):
     """A NaN or infinite query makes its own row NaN; a NaN key or value reaches exactly the rows (and, for a value, the
