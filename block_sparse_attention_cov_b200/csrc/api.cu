@@ -276,11 +276,14 @@ int solattn_dense(const void* q, const void* k, const void* v, int B, int H, int
 
 #ifdef SOLATTN_TEST_HOOKS
 // Test builds only (libsolattn_testhooks.so; not declared in include/solattn.h):
-// CTA `skip_cta` never requests its first K tile (-1: none) and every bounded
+// CTA `skip_cta` never requests its first K tile (the cache kernels: the CTAs of
+// that x index their first page; -1: none) and every bounded
 // wait gives up after `wait_budget_ns`.
 int solattn_test_set_hook(int skip_cta, unsigned long long wait_budget_ns) {
   const bool ok = solattn::set_test_hooks_fwd(skip_cta, wait_budget_ns) == cudaSuccess &&
-                  solattn::set_test_hooks_pp(skip_cta, wait_budget_ns) == cudaSuccess;
+                  solattn::set_test_hooks_pp(skip_cta, wait_budget_ns) == cudaSuccess &&
+                  solattn::set_test_hooks_step(skip_cta, wait_budget_ns) == cudaSuccess &&
+                  solattn::set_test_hooks_chunk(skip_cta, wait_budget_ns) == cudaSuccess;
   return ok ? SOLATTN_OK : SOLATTN_ERR_CUDA;
 }
 

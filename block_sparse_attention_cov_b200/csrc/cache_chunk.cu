@@ -451,6 +451,9 @@ __global__ void __launch_bounds__(kChunkThreads, 1) cache_chunk_kernel(const Cac
           const float2 kv = make_float2(__shfl_sync(0xffffffffu, ks, i), __shfl_sync(0xffffffffu, vs, i));
           if (p >= kRaw)
             ok = chunk_wait(&sm.raw_empty[s], ((p / kRaw) & 1) ^ 1, abort_flag, st, kSiteCRawEmpty, blockIdx.x);
+#ifdef SOLATTN_TEST_HOOKS
+          if (p == 0 && static_cast<int>(blockIdx.x) == g_hook_skip_cta) continue;  // this page never arrives
+#endif
           if (ok && lane == 0) {
             // the scales' slot held page p - 8: page p - 2 has been converted, so the QK of page p - 6 is
             // complete, and it was issued behind P of page p - 8 in both tiles
@@ -699,6 +702,14 @@ cudaError_t launch_chunk_t(const CacheAttnArgs& a, cudaStream_t stream) {
 }
 
 }  // namespace
+
+#ifdef SOLATTN_TEST_HOOKS
+cudaError_t set_test_hooks_chunk(int skip_cta, unsigned long long wait_budget_ns) {
+  cudaError_t e = cudaMemcpyToSymbol(g_hook_skip_cta, &skip_cta, sizeof(skip_cta));
+  if (e == cudaSuccess) e = cudaMemcpyToSymbol(g_wait_budget_ns, &wait_budget_ns, sizeof(wait_budget_ns));
+  return e;
+}
+#endif
 
 cudaError_t launch_cache_chunk(const CacheAttnArgs& a, cudaStream_t stream) {
   if (a.dtype == kF16)

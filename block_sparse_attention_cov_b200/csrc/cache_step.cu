@@ -139,6 +139,9 @@ __global__ void __launch_bounds__((kWarps + 1) * 32, 3)
       // the first pages' copies go out before their scales have come
       const int ahead = base == c0 ? min(count, ST) : 0;
       auto issue = [&](int n, int page) {
+#ifdef SOLATTN_TEST_HOOKS
+        if (n == 0 && static_cast<int>(blockIdx.x) == g_hook_skip_cta) return;  // this page never arrives
+#endif
         if (lane == 0) {
           const int s = n % ST;
           if (page >= 0) {
@@ -546,6 +549,14 @@ cudaError_t launch_join_t(const CacheAttnArgs& a, cudaStream_t stream) {
 }
 
 }  // namespace
+
+#ifdef SOLATTN_TEST_HOOKS
+cudaError_t set_test_hooks_step(int skip_cta, unsigned long long wait_budget_ns) {
+  cudaError_t e = cudaMemcpyToSymbol(g_hook_skip_cta, &skip_cta, sizeof(skip_cta));
+  if (e == cudaSuccess) e = cudaMemcpyToSymbol(g_wait_budget_ns, &wait_budget_ns, sizeof(wait_budget_ns));
+  return e;
+}
+#endif
 
 cudaError_t launch_cache_step(const CacheAttnArgs& a, cudaStream_t stream) {
   if (a.dtype == kF16) return a.d == 64 ? launch_step_t<__half, 64>(a, stream) : launch_step_t<__half, 128>(a, stream);

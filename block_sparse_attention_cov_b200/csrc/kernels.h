@@ -147,6 +147,8 @@ cudaError_t launch_cache_join(const CacheAttnArgs& a, cudaStream_t stream);
 cudaError_t set_test_hooks_fwd(int skip_cta, unsigned long long wait_budget_ns);
 cudaError_t set_route_dump_fwd(uint32_t* mask, float* stats);
 cudaError_t set_test_hooks_pp(int skip_cta, unsigned long long wait_budget_ns);
+cudaError_t set_test_hooks_step(int skip_cta, unsigned long long wait_budget_ns);
+cudaError_t set_test_hooks_chunk(int skip_cta, unsigned long long wait_budget_ns);
 cudaError_t set_route_dump_pp(uint32_t* mask, float* stats);
 #endif
 
