@@ -253,3 +253,22 @@ def test_rotary_pool_then_forward():
     top = float(sep.view("vbar").abs().max())
     assert (a.float() - b.float()).abs().max() <= 2.5 * delta * top + 2 * 2.0 ** -9 * top
     assert (la - lb).abs().max() <= delta + 1e-5
+
+
+@pytest.mark.parametrize("dtype", [torch.bfloat16, torch.float16, torch.float32])
+@pytest.mark.parametrize("layout", ["half", "interleaved"])
+@pytest.mark.parametrize("d,rot", [(72, 64), (128, 16), (128, 96), (88, 32), (64, 6)])
+def test_what_is_behind_the_rotated_part_keeps_its_bits(d, rot, layout, dtype):
+    """Any bits behind the rotated part (NaN payloads, infinities) are copied; the part before takes none of them."""
+    g = torch.Generator().manual_seed(31)
+    as_int = torch.int32 if dtype == torch.float32 else torch.int16
+    info = torch.iinfo(as_int)
+    x = _rand((2, 3, 21, d), dtype, 32)
+    x[..., rot:] = torch.randint(info.min, info.max + 1, (2, 3, 21, d - rot), generator=g,
+                                 dtype=torch.int64).to(as_int).cuda().view(dtype)
+    pos = torch.arange(21, dtype=torch.int32, device="cuda") * 97
+    y, _ = sa.rotary(x, None, sa.Rotary(rot, layout=layout), pos)
+    assert torch.equal(y[..., rot:].contiguous().view(as_int), x[..., rot:].contiguous().view(as_int))
+    freq, axis, gain = ref.frequencies([rot // 2])
+    _check(y[..., :rot], x[..., :rot], ref.rotate(x[..., :rot], pos.cpu()[None, :, None], freq, axis, rot, layout),
+           rot, layout, 1.0)
