@@ -1,5 +1,5 @@
 // cache_chunk.cu -- attention of many queries (a prompt, a chunk, a video frame)
-// over the 8-bit cache, on tcgen05.
+// over the 8-bit cache, on tcgen05, where that is estimated to be the faster.
 //
 // One CTA takes 256 query rows of one key head (token-major, the heads of the
 // group side by side) as two 128-row tiles, and one part of the keys. Both tiles

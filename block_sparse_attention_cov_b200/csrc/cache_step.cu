@@ -1,5 +1,5 @@
-// cache_step.cu -- attention of a few queries (a decoding step) over the 8-bit
-// cache, and the kernel that joins partial results of a split key axis.
+// cache_step.cu -- attention of a few queries (a decoding step), or of more over a
+// short cache, and the kernel that joins partial results of a split key axis.
 //
 // cache_step_kernel is bound by reading the cache: 2 d bytes per key and head
 // against 4 d flops per query row. One CTA takes up to 16 rows (query heads of

@@ -129,7 +129,8 @@ int solattn_rotary_frequencies(int rot, int axes, const int* pairs, double theta
   int at = 0;
   for (int a = 0; a < axes; ++a) {
     const double n = count[a];
-    const double base = scaling == SOLATTN_SCALING_NTK && count[a] > 1 ? theta * std::pow(factor, 2 * n / (2 * n - 2)) : theta;
+    const bool ntk = scaling == SOLATTN_SCALING_NTK && count[a] > 1;
+    const double base = ntk ? theta * std::pow(factor, 2 * n / (2 * n - 2)) : theta;
     for (int i = 0; i < count[a]; ++i, ++at) {
       double f = std::pow(base, -i / n);
       if (scaling == SOLATTN_SCALING_LINEAR) f /= factor;
@@ -337,26 +338,41 @@ int solattn_cache_attention(const void* q, int dtype, int B, int H, int N, int d
 
 }  // extern "C"
 
+#ifdef SOLATTN_TEST_HOOKS
+// Test builds only: 1 takes the kernel of few rows for every call that fits its
+// grid, 2 the kernel of many rows, 0 what the estimates say.
+static int g_hook_cache_kernel = 0;
+extern "C" void solattn_test_set_cache_kernel(int which) { g_hook_cache_kernel = which; }
+#endif
+
 namespace solattn {
 
+// Estimates in microseconds of the two attention kernels, each at the number of
+// parts of the key axis that it does best with; the cheaper one is launched.
+// Rows of one key head go in tiles of 16 that read the cache once each, or in
+// tiles of 256 on tcgen05: the first starts and finishes sooner and spreads short
+// calls over more CTAs, the second reads and converts the cache 16 times less.
+// 300 queries x 4 heads, 500 keys: 8.4 and 17.7 us; 2 x 285 queries of 20 heads
+// (4 key heads), 900 keys: 39.5 and 32.3 us; 64 key heads of 16384 tokens: 32 rows
+// 179 and 278 us, 48 rows 257 and 280, 64 rows 331 and 280. Over 70 calls drawn
+// between 49 and 12000 rows and 2 and 8000 keys the estimates took the faster one
+// each time, 1.29 times faster than the second alone.
 CachePlan cache_plan(int B, int H, int Hk, int N, int d, int columns) {
   constexpr int kSms = 148;
   const long long rows = static_cast<long long>(N) * (H / Hk);
-  // Rows of one key head in tiles of 16 that read the cache once each, or in tiles
-  // of 256 on tcgen05. 64 key heads of 16384 tokens: 32 rows 179 and 278 us, 48 rows
-  // 257 and 280 us, 64 rows 331 and 280 us.
-  CachePlan p{rows <= 48, 1};
   auto ceil_div = [](long long x, long long y) { return (x + y - 1) / y; };
-  if (p.step) {
+  CachePlan step{true, 1}, chunk{false, 1};
+  double step_cost = 0, chunk_cost = 0;
+  {
     // Three CTAs per SM: a part costs about 5 us to start and finish and 0.75 us
     // per page, all parts together what memory gives (5.9 TB/s, and the start of
     // every wave but the first); among several sequences, which differ in length,
-    // some of a part is left at the end. Counts that fill one to eight waves are compared: 8 key heads of 65536 tokens
-    // take 33 us in 37 parts, 43 us in 74; 32 sequences of 32000 tokens take 388 us
-    // whole, 352 us in 3 parts; of 8000 to 32700 tokens 373 us, 231 us in 8.
+    // some of a part is left at the end. Counts that fill one to eight waves are
+    // compared: 8 key heads of 65536 tokens take 33 us in 37 parts, 43 us in 74; 32
+    // sequences of 32000 tokens take 388 us whole, 352 us in 3 parts; of 8000 to
+    // 32700 tokens 373 us, 231 us in 8.
     const long long units = static_cast<long long>(B) * Hk * ceil_div(rows, 16);
     const double memory = static_cast<double>(units) * columns * 128 * d / 5.9e6;
-    double best = 0;
     for (int w = 0; w <= 8; ++w) {
       const long long s = w == 0 ? 1 : std::min<long long>(3ll * kSms * w / units, columns);
       if (s < 1) continue;
@@ -364,12 +380,13 @@ CachePlan cache_plan(int B, int H, int Hk, int N, int d, int columns) {
       const double part = 5 + 0.75 * ceil_div(columns, s);
       const long long waves = ceil_div(units * s, 3 * kSms);
       const double cost = std::max(waves * part, memory + 5 * (waves - 1)) + join + (B > 1 ? 0.15 * part : 0);
-      if (w == 0 || cost < best) {
-        best = cost;
-        p.splits = static_cast<int>(s);
+      if (w == 0 || cost < step_cost) {
+        step_cost = cost;
+        step.splits = static_cast<int>(s);
       }
     }
-  } else {
+  }
+  {
     // One CTA per SM: a part of the key axis costs about 9 us to start and finish
     // and 2.5 us per key tile (two pages), parts run in waves of 148, and what is
     // joined is written and read once at about 6 TB/s. The split with the least
@@ -378,17 +395,21 @@ CachePlan cache_plan(int B, int H, int Hk, int N, int d, int columns) {
     // the GPU by their upper bounds the key axis stays whole: shorter sequences
     // leave fewer CTAs than that (3 of up to 1111 queries: 62 us, 95 us in 2).
     const long long units = static_cast<long long>(B) * Hk * ceil_div(rows, 256), tiles = ceil_div(columns, 2);
-    double best = 0;
     for (int s = 1; s <= 16 && (s == 1 || (s * 2 <= tiles && (B == 1 || units < kSms))); ++s) {
       const double join = s == 1 ? 0 : 3 + static_cast<double>(B) * H * N * s * d * 8 / 6e6;
       const double cost = ceil_div(units * s, kSms) * (9 + 2.5 * ceil_div(tiles, s)) + join;
-      if (s == 1 || cost < best) {
-        best = cost;
-        p.splits = s;
+      if (s == 1 || cost < chunk_cost) {
+        chunk_cost = cost;
+        chunk.splits = s;
       }
     }
   }
-  return p;
+  const bool fits = ceil_div(rows, 16) * Hk <= 65535;  // the first kernel's grid
+#ifdef SOLATTN_TEST_HOOKS
+  if (g_hook_cache_kernel == 1 && fits) return step;
+  if (g_hook_cache_kernel == 2) return chunk;
+#endif
+  return fits && step_cost <= chunk_cost ? step : chunk;
 }
 
 }  // namespace solattn
