@@ -207,12 +207,14 @@ __device__ __forceinline__ void st_shared_v4(void* p, uint32_t a, uint32_t b, ui
 
 // 32 rows of queries into the operand layout, scaled to fp16's range by a power
 // of two per row: copied as they are (a row's lanes side by side, so that a copy
-// touches a few lines and not one per lane), then every lane converts one row in
-// place. Returns the factor of the lane's row. The loops are short on purpose:
-// they run once, and what is unrolled is first fetched.
-template <typename Elem, int D>
-__device__ __forceinline__ float load_queries(const CacheAttnArgs& a, uint8_t* tile, int b, int hk, int first, int rows,
-                                              int wq, int lane) {
+// touches a few lines and not one per lane; before the sequence's counts are
+// read, so rows of the tensor behind them too), then every lane converts one row
+// in place, a row that is not there to zeros, and returns its factor. The loops
+// are short on purpose: they run once, and what is unrolled is first fetched.
+template <int D>
+__device__ __forceinline__ void copy_queries(const CacheAttnArgs& a, uint8_t* tile, int b, int hk, int first, int wq,
+                                             int lane) {
+  const int rows = a.N * a.group;
   constexpr int LPR = D / 8, RPL = 32 / LPR;  // lanes per row, rows per step
   const int ch = lane % LPR;
   uint8_t* to = tile + (ch / 8) * (kTileRows * 128);
@@ -226,7 +228,13 @@ __device__ __forceinline__ float load_queries(const CacheAttnArgs& a, uint8_t* t
                  "l"(r < rows ? from + g * a.st.h + qi * a.st.n : a.q), "r"(r < rows ? 16 : 0)
                  : "memory");
   }
-  asm volatile("cp.async.wait_all;" ::: "memory");
+}
+
+// Every copy of the thread has landed.
+__device__ __forceinline__ void copies_done() { asm volatile("cp.async.wait_all;" ::: "memory"); }
+
+template <typename Elem, int D>
+__device__ __forceinline__ float convert_queries(uint8_t* tile, bool there, int wq, int lane) {
   __syncwarp();
   const int lr = wq * 32 + lane;
   uint8_t* row = tile + lr * 128;
@@ -243,7 +251,7 @@ __device__ __forceinline__ float load_queries(const CacheAttnArgs& a, uint8_t* t
 #pragma unroll 2
   for (int c = 0; c < D / 8; ++c) {
     uint4* p = reinterpret_cast<uint4*>(row + (c / 8) * (kTileRows * 128) + ((c % 8 * 16) ^ x));
-    const uint4 w = *p;
+    const uint4 w = there ? *p : make_uint4(0, 0, 0, 0);
     const float2 f0 = unpack2<Elem>(w.x), f1 = unpack2<Elem>(w.y), f2 = unpack2<Elem>(w.z), f3 = unpack2<Elem>(w.w);
     *p = make_uint4(pack_f16x2(f0.x * mul, f0.y * mul), pack_f16x2(f1.x * mul, f1.y * mul),
                     pack_f16x2(f2.x * mul, f2.y * mul), pack_f16x2(f3.x * mul, f3.y * mul));
@@ -296,7 +304,9 @@ __global__ void __launch_bounds__(kChunkThreads, 1) cache_chunk_kernel(const Cac
   DeviceStatus* st = a.status;
   volatile int* abort_flag = &sm.abort_flag;
   start_join(a);
-  if (tid == 0) {
+  const int r0 = mt * 2 * kTileRows;
+  if (warp < 8) copy_queries<D>(a, sm.q[warp / 4], b, hk, r0 + warp / 4 * kTileRows, warp % 4, lane);
+  if (tid == kChunkThreads - 32) {  // a warp with nothing else to do
     for (int i = 0; i < kKStages; ++i) {
       mbar_init(&sm.k_full[i], 8);  // four warps, two pages
       mbar_init(&sm.k_empty[i], 1);
@@ -314,7 +324,7 @@ __global__ void __launch_bounds__(kChunkThreads, 1) cache_chunk_kernel(const Cac
     }
     for (int i = 0; i < 2; ++i) mbar_init(&sm.q_full[i], 4);
     for (int i = 0; i < kRaw; ++i) {
-      mbar_init(&sm.raw_full[i], 1);
+      mbar_init(&sm.raw_full[i], 2);  // the copies' issue and the scales
       mbar_init(&sm.raw_empty[i], 4);
     }
     mbar_init(&sm.mma_done, 1);
@@ -325,8 +335,10 @@ __global__ void __launch_bounds__(kChunkThreads, 1) cache_chunk_kernel(const Cac
   __syncthreads();
   const Extent ex = extent(a, b, split == 0 && hk == 0 && mt == 0 && tid == 0);
   const int rows = ex.cnt * a.group;
-  const int r0 = mt * 2 * kTileRows;
-  if (r0 >= rows) return;  // rows behind the sequence's queries stay as they are
+  if (r0 >= rows) {  // rows behind the sequence's queries stay as they are
+    copies_done();
+    return;
+  }
   const int nq = rows - r0 > kTileRows ? 2 : 1;  // 128-row tiles with rows in them
   const int last_row = min(rows, r0 + 2 * kTileRows) - 1;
   const int seen = key_limit(ex, a.causal, last_row / a.group);  // keys that some row sees
@@ -445,19 +457,12 @@ __global__ void __launch_bounds__(kChunkThreads, 1) cache_chunk_kernel(const Cac
             vs = __ldg(a.v_scale + pg * a.scale_stride + hk);
           }
         }
-        for (int i = 0; i < min(32, P - base) && ok; ++i) {
-          const int p = base + i, s = p % kRaw;
-          const int page = __shfl_sync(0xffffffffu, pg, i);
-          const float2 kv = make_float2(__shfl_sync(0xffffffffu, ks, i), __shfl_sync(0xffffffffu, vs, i));
-          if (p >= kRaw)
-            ok = chunk_wait(&sm.raw_empty[s], ((p / kRaw) & 1) ^ 1, abort_flag, st, kSiteCRawEmpty, blockIdx.x);
+        auto issue = [&](int p, int page) {
 #ifdef SOLATTN_TEST_HOOKS
-          if (p == 0 && static_cast<int>(blockIdx.x) == g_hook_skip_cta) continue;  // this page never arrives
+          if (p == 0 && static_cast<int>(blockIdx.x) == g_hook_skip_cta) return;  // this page never arrives
 #endif
-          if (ok && lane == 0) {
-            // the scales' slot held page p - 8: page p - 2 has been converted, so the QK of page p - 6 is
-            // complete, and it was issued behind P of page p - 8 in both tiles
-            sm.info[p % kInfo] = kv;
+          if (lane == 0) {
+            const int s = p % kRaw;
             if (page >= 0) {
               const long long at = page * a.page_stride + static_cast<long long>(hk) * kPage * D;
               mbar_arrive_expect_tx(&sm.raw_full[s], 2 * kPage * D);
@@ -466,7 +471,26 @@ __global__ void __launch_bounds__(kChunkThreads, 1) cache_chunk_kernel(const Cac
             } else {
               mbar_arrive(&sm.raw_full[s]);
             }
-            issued = p + 1;
+          }
+          issued = p + 1;
+        };
+        // the first pages' copies go out before their scales have come
+        const int ahead = base == 0 ? min(kRaw, P) : 0;
+        for (int i = 0; i < ahead; ++i) issue(i, __shfl_sync(0xffffffffu, pg, i));
+        for (int i = 0; i < min(32, P - base) && ok; ++i) {
+          const int p = base + i, s = p % kRaw;
+          const int page = __shfl_sync(0xffffffffu, pg, i);
+          if (i >= ahead) {
+            ok = chunk_wait(&sm.raw_empty[s], ((p / kRaw) & 1) ^ 1, abort_flag, st, kSiteCRawEmpty, blockIdx.x);
+            if (!ok) break;
+            issue(p, page);
+          }
+          const float2 kv = make_float2(__shfl_sync(0xffffffffu, ks, i), __shfl_sync(0xffffffffu, vs, i));
+          if (lane == 0) {
+            // the scales' slot held page p - 8: page p - 2 has been converted, so the QK of page p - 6 is
+            // complete, and it was issued behind P of page p - 8 in both tiles
+            sm.info[p % kInfo] = kv;
+            mbar_arrive(&sm.raw_full[s]);
           }
           __syncwarp();
         }
@@ -548,6 +572,7 @@ __global__ void __launch_bounds__(kChunkThreads, 1) cache_chunk_kernel(const Cac
     }
   } else {
     regs_inc<152>();
+    copies_done();
     if (warp / 4 < nq) {
       // ======================= softmax =======================
       const int x = warp / 4, wq = warp % 4;
@@ -559,7 +584,7 @@ __global__ void __launch_bounds__(kChunkThreads, 1) cache_chunk_kernel(const Cac
       const int h = hk * a.group + g;
       const int lim = there ? key_limit(ex, a.causal, qi) : seen;  // a row that is not there masks nothing by itself
       const uint32_t lane_sel = static_cast<uint32_t>(wq * 32) << 16;
-      const float rf = load_queries<Elem, D>(a, sm.q[x], b, hk, r0 + x * kTileRows, rows, wq, lane);
+      const float rf = convert_queries<Elem, D>(sm.q[x], there, wq, lane);
       if (lane == 0) mbar_arrive(&sm.q_full[x]);
       uint32_t colS = 0, colO = 0;
       float m = -INFINITY, l = 0.f;
@@ -592,6 +617,13 @@ __global__ void __launch_bounds__(kChunkThreads, 1) cache_chunk_kernel(const Cac
         // P with the reference as it stands, beside the maximum rather than behind
         // it; only a page that passes the reference by kSlack (rare after the first
         // ones) is done again
+        // No reference yet: the maximum first, or every row would do the page again.
+        // Worth 0.6 us of a short call; at d = 128 the loop's code with it costs long
+        // calls 5 % (256 x 8192 x 148 heads: 147 to 155 us).
+        if (kPageSlots && p == 0) {
+          const float tm = fmaf(page_max(sv), c, ps.ev);
+          if (tm > -INFINITY) m = ceilf(tm);
+        }
         float sum;
         while (true) {
           sum = page_weights<kPolyEvery>(sv, c, page_addend(ps, m), pw);
