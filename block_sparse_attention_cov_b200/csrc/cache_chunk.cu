@@ -300,7 +300,7 @@ __global__ void __launch_bounds__(kChunkThreads, 1) cache_chunk_kernel(const Cac
   const int tid = threadIdx.x, warp = tid / 32, lane = tid % 32;
   // the tiles that see most keys first
   const int split = blockIdx.x % a.splits, mt = tiles - 1 - blockIdx.x / a.splits;
-  const int hk = blockIdx.y, b = blockIdx.z;
+  const int hk = blockIdx.y, b = a.longest_first ? nth_longest(a, blockIdx.z, lane) : blockIdx.z;
   DeviceStatus* st = a.status;
   volatile int* abort_flag = &sm.abort_flag;
   start_join(a);

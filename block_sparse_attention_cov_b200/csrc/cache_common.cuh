@@ -25,6 +25,7 @@
 #include <cuda_bf16.h>
 #include <cuda_fp16.h>
 #include <cuda_runtime.h>
+#include <climits>
 #include <cstdint>
 
 #include "kernels.h"
@@ -57,6 +58,30 @@ __device__ __forceinline__ Extent extent(const CacheAttnArgs& a, int b, bool rep
   e.cnt = cnt < 0 ? 0 : (cnt > a.N ? a.N : cnt);
   if (report && (e.len != len || e.cnt != cnt)) report_page(a.status, b);
   return e;
+}
+
+// The sequence that is the n-th longest (of equals, the first): a call of several
+// waves that takes the long sequences first ends more evenly. B <= 64; every lane
+// of a warp calls it and gets the same answer.
+__device__ __forceinline__ int nth_longest(const CacheAttnArgs& a, int n, int lane) {
+  const int v0 = lane < a.B ? __ldg(a.lengths + lane) : INT_MIN;
+  const int v1 = lane + 32 < a.B ? __ldg(a.lengths + lane + 32) : INT_MIN;
+  int r0 = 0, r1 = 0;
+#pragma unroll 4
+  for (int j = 0; j < min(a.B, 32); ++j) {
+    const int w = __shfl_sync(0xffffffffu, v0, j);
+    r0 += w > v0 || (w == v0 && j < lane);
+    r1 += w >= v1;
+  }
+#pragma unroll 4
+  for (int j = 32; j < a.B; ++j) {
+    const int w = __shfl_sync(0xffffffffu, v1, j - 32);
+    r0 += w > v0;
+    r1 += w > v1 || (w == v1 && j < lane + 32);
+  }
+  const unsigned int m0 = __ballot_sync(0xffffffffu, lane < a.B && r0 == n);
+  const unsigned int m1 = __ballot_sync(0xffffffffu, lane + 32 < a.B && r1 == n);
+  return m0 ? __ffs(m0) - 1 : 31 + __ffs(m1);
 }
 
 // Query token and head within its group of a row (token-major).

@@ -81,7 +81,8 @@ __global__ void __launch_bounds__((kWarps + 1) * 32, 3)
   Smem& sm = *reinterpret_cast<Smem*>(smem_raw + ((1024u - (smem_u32(smem_raw) & 1023u)) & 1023u));
   const int tid = threadIdx.x, warp = tid / 32, lane = tid % 32;
   const int g = lane / 4, t = lane % 4;
-  const int split = blockIdx.x, b = blockIdx.z;
+  const int split = blockIdx.x;
+  const int b = a.longest_first ? nth_longest(a, blockIdx.z, lane) : blockIdx.z;
   const int hk = blockIdx.y % a.Hk, tile = blockIdx.y / a.Hk;
   DeviceStatus* st = a.status;
   volatile int* abort_flag = &sm.abort_flag;

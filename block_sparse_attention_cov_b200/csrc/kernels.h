@@ -128,6 +128,7 @@ struct CacheAttnArgs {
   uint32_t group_shift;
   int causal;
   int splits;             // parts of the key axis, joined from part_o / part_ml when > 1
+  int longest_first;      // the grid takes the sequences by falling length (B <= 64)
   float* part_o;          // [B][H][N][splits][d]
   float2* part_ml;        // [B][H][N][splits] (reference, sum)
   DeviceStatus* status;
@@ -136,6 +137,7 @@ struct CacheAttnArgs {
 struct CachePlan {
   bool step;
   int splits;
+  bool longest_first;
 };
 CachePlan cache_plan(int B, int H, int Hk, int N, int d, int columns);
 cudaError_t launch_cache_step(const CacheAttnArgs& a, cudaStream_t stream);

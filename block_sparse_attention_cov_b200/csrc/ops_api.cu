@@ -326,6 +326,7 @@ int solattn_cache_attention(const void* q, int dtype, int B, int H, int N, int d
   a.group_mul = static_cast<uint32_t>((1ull << 32) * ((1ull << a.group_shift) - a.group) / a.group + 1);
   a.causal = causal != 0;
   a.splits = plan.splits;
+  a.longest_first = plan.longest_first;
   char* ws = static_cast<char*>(workspace) + SOLATTN_WORKSPACE_BYTES;
   a.part_o = reinterpret_cast<float*>(ws);
   a.part_ml = reinterpret_cast<float2*>(a.part_o + static_cast<size_t>(B) * H * N * plan.splits * d);
@@ -361,7 +362,7 @@ CachePlan cache_plan(int B, int H, int Hk, int N, int d, int columns) {
   constexpr int kSms = 148;
   const long long rows = static_cast<long long>(N) * (H / Hk);
   auto ceil_div = [](long long x, long long y) { return (x + y - 1) / y; };
-  CachePlan step{true, 1}, chunk{false, 1};
+  CachePlan step{true, 1, false}, chunk{false, 1, false};
   double step_cost = 0, chunk_cost = 0;
   {
     // Three CTAs per SM: a part costs about 5 us to start and finish and 0.75 us
@@ -379,10 +380,11 @@ CachePlan cache_plan(int B, int H, int Hk, int N, int d, int columns) {
       const double join = s == 1 ? 0 : 2 + static_cast<double>(B) * H * N * s * d * 8 / 6e6;
       const double part = 5 + 0.75 * ceil_div(columns, s);
       const long long waves = ceil_div(units * s, 3 * kSms);
-      const double cost = std::max(waves * part, memory + 5 * (waves - 1)) + join + (B > 1 ? 0.15 * part : 0);
+      const double cost = std::max(waves * part, memory + 5 * (waves - 1)) + join + (B > 1 ? 0.3 * part : 0);
       if (w == 0 || cost < step_cost) {
         step_cost = cost;
         step.splits = static_cast<int>(s);
+        step.longest_first = B > 1 && B <= 64 && waves > 1;
       }
     }
   }
@@ -401,9 +403,15 @@ CachePlan cache_plan(int B, int H, int Hk, int N, int d, int columns) {
       if (s == 1 || cost < chunk_cost) {
         chunk_cost = cost;
         chunk.splits = s;
+        chunk.longest_first = B > 1 && B <= 64 && units * s > kSms;
       }
     }
   }
+  // Calls of several waves over several sequences take the long ones first, so
+  // that what is left at the end is short (every CTA ranks the lengths, two per
+  // lane, hence 64 sequences at most): 32 sequences of 8000 to 32700 tokens 249 to
+  // 209 us, 8 of 1000 to 8000 with 500 queries 232 to 217 us; equal lengths are
+  // not slower (334 and 331 us).
   const bool fits = ceil_div(rows, 16) * Hk <= 65535;  // the first kernel's grid
 #ifdef SOLATTN_TEST_HOOKS
   if (g_hook_cache_kernel == 1 && fits) return step;

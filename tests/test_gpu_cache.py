@@ -170,6 +170,18 @@ def test_attention_long_table_short_sequences(N):
         _check_attention(q, c, t, vals, lengths, counts, causal, out, lse)
 
 
+@pytest.mark.parametrize("B,Hk,N", [(33, 16, 1), (64, 8, 1), (65, 8, 1), (33, 16, 3)])
+def test_attention_of_many_sequences(B, Hk, N):
+    """More key heads than the GPU takes at once, sequences of equal, falling, rising and no length, with and without
+    queries: each gets its own answer."""
+    lengths = [(37 * b) % 150 if b % 5 else (0, 64, 150)[b % 3] for b in range(B)]
+    counts = [min(n, N if b % 7 else 0) for b, n in enumerate(lengths)]
+    c, t, vals = _filled(lengths, Hk, 64, seed=B + N)
+    q = torch.randn((B, 2 * Hk, N, 64), generator=_gen(15)).to(torch.bfloat16).cuda()
+    out, lse = _attend(q, c, t, lengths, counts, True)
+    _check_attention(q, c, t, vals, lengths, counts, True, out, lse)
+
+
 @pytest.mark.parametrize("N", [1, 90])
 @pytest.mark.parametrize("size", [1e-30, 30.0, 1e4])
 def test_attention_extreme_queries_and_scales(N, size):

@@ -7,7 +7,7 @@ from block_sparse_attention_cov_b200.build import build
 from hooklib import hooks_lib
 from test_gpu_cache import (  # noqa: F401
     test_attention_against_formula, test_attention_extreme_queries_and_scales,
-    test_attention_long_table_short_sequences, test_attention_not_finite, test_attention_of_zero_queries_and_zero_values,
+    test_attention_long_table_short_sequences, test_attention_not_finite, test_attention_of_many_sequences, test_attention_of_zero_queries_and_zero_values,
     test_attention_strides_streams_and_repeats, test_bad_pages_lengths_and_counts_are_reported_and_touch_nothing,
     test_every_e4m3_value_is_read_exactly, test_rows_that_see_nothing_at_any_value_scale,
     test_together_as_a_decoder_uses_them)
