@@ -287,6 +287,11 @@ __device__ __forceinline__ void store_rows(const CacheAttnArgs& a, const uint8_t
   __syncwarp();
 }
 
+// Out of line: in the kernel its registers cost the softmax loop 3 %.
+static __device__ __noinline__ int ranked_sequence(const CacheAttnArgs& a, int n, int lane) {
+  return nth_longest(a, n, lane);
+}
+
 template <typename Elem, int D>
 __global__ void __launch_bounds__(kChunkThreads, 1) cache_chunk_kernel(const CacheAttnArgs a, int tiles) {
   constexpr bool kPageSlots = D == 64;
@@ -300,7 +305,7 @@ __global__ void __launch_bounds__(kChunkThreads, 1) cache_chunk_kernel(const Cac
   const int tid = threadIdx.x, warp = tid / 32, lane = tid % 32;
   // the tiles that see most keys first
   const int split = blockIdx.x % a.splits, mt = tiles - 1 - blockIdx.x / a.splits;
-  const int hk = blockIdx.y, b = a.longest_first ? nth_longest(a, blockIdx.z, lane) : blockIdx.z;
+  const int hk = blockIdx.y, b = a.longest_first ? ranked_sequence(a, blockIdx.z, lane) : blockIdx.z;
   DeviceStatus* st = a.status;
   volatile int* abort_flag = &sm.abort_flag;
   start_join(a);

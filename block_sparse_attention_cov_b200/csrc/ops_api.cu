@@ -370,8 +370,7 @@ CachePlan cache_plan(int B, int H, int Hk, int N, int d, int columns) {
     // every wave but the first); among several sequences, which differ in length,
     // some of a part is left at the end. Counts that fill one to eight waves are
     // compared: 8 key heads of 65536 tokens take 33 us in 37 parts, 43 us in 74; 32
-    // sequences of 32000 tokens take 388 us whole, 352 us in 3 parts; of 8000 to
-    // 32700 tokens 373 us, 231 us in 8.
+    // sequences of 32000 tokens take 388 us whole, 331 us in 5 parts.
     const long long units = static_cast<long long>(B) * Hk * ceil_div(rows, 16);
     const double memory = static_cast<double>(units) * columns * 128 * d / 5.9e6;
     for (int w = 0; w <= 8; ++w) {
@@ -410,7 +409,7 @@ CachePlan cache_plan(int B, int H, int Hk, int N, int d, int columns) {
   // Calls of several waves over several sequences take the long ones first, so
   // that what is left at the end is short (every CTA ranks the lengths, two per
   // lane, hence 64 sequences at most): 32 sequences of 8000 to 32700 tokens 249 to
-  // 209 us, 8 of 1000 to 8000 with 500 queries 232 to 217 us; equal lengths are
+  // 209 us, 8 of 1000 to 8000 with 500 queries 232 to 206 us; equal lengths are
   // not slower (334 and 331 us).
   const bool fits = ceil_div(rows, 16) * Hk <= 65535;  // the first kernel's grid
 #ifdef SOLATTN_TEST_HOOKS
