@@ -657,10 +657,13 @@ __global__ void __launch_bounds__(kChunkThreads, 1) cache_chunk_kernel(const Cac
         ok = chunk_wait<1>(&sm.pv_done[x][(P - 1) & 1], ((P - 1) >> 1) & 1, abort_flag, st, kSiteCPv, blockIdx.x);
         tc_fence_after();
       }
+      // Without a page no QK stands between a warp's queries and another warp's
+      // stage below, which lies over them.
+      if (P == 0) named_bar_sync(1 + x, kTileRows);
       if (ok) {
         // ---- the row's result, or its part. A warp's 32 rows go through its
-        // quarter of the Q tile (its last QK is complete) 64 columns at a time, so
-        // that the stores run along rows, a few lines each.
+        // quarter of the Q tile (its last QK is complete, or there was none) 64
+        // columns at a time, so that the stores run along rows, a few lines each.
         const bool part = a.splits > 1;
         const float inv = part ? 1.f : (l != 0.f ? 1.f / l : 0.f);
         const long long pr = partial_row(a, b, h, qi, split);
