@@ -62,7 +62,9 @@ struct __align__(1024) ChunkSmem {
   uint8_t k[kKStages][kTileKeys * D * 2]; // the same
   uint8_t v[kVStages][kPage * D * 2];     // SW128 panels of 64 rows
   uint8_t raw[kRaw][2][kPage * D];        // keys and values of a page, e4m3
-  float2 info[kInfo];                     // scales of a page's keys and values
+  float4 info[kInfo];                     // a page's factors (PageScale), and kSlack: NaN where the unit changes
+  float turn[kInfo];                      // what O is multiplied by before the page
+  int unit;                               // of the last page, as its exponent
   uint64_t q_full[2], k_full[kKStages], k_empty[kKStages], v_full[kVStages], v_empty[kVStages];
   uint64_t raw_full[kRaw], raw_empty[kRaw];
   uint64_t s_full[2][2], p_full[2][2], pv_done[2][2], mma_done;
@@ -167,7 +169,7 @@ __device__ __forceinline__ float page_weights(const uint32_t (&sv)[64], float c,
 __device__ __forceinline__ float row_scale(const PageScale& ps, float rf) { return fmaxf(ps.ck * rf, 1.17549435e-38f); }
 // The exponent's addend of a page for a row with reference m.
 __device__ __forceinline__ float page_addend(const PageScale& ps, float m) {
-  return ps.vinv == 0.f ? -INFINITY : ps.ev + kPBias - (m == -INFINITY ? 0.f : m);
+  return ps.ev == -INFINITY ? -INFINITY : ps.ev + kPBias - (m == -INFINITY ? 0.f : m);
 }
 
 // Rare paths, out of line; warp-collective, a lane with factor 1 keeps its row.
@@ -333,6 +335,7 @@ __global__ void __launch_bounds__(kChunkThreads, 1) cache_chunk_kernel(const Cac
       mbar_init(&sm.raw_empty[i], 4);
     }
     mbar_init(&sm.mma_done, 1);
+    sm.unit = 127;
     sm.abort_flag = 0;
     sm.nan = 0;
     fence_barrier_init();
@@ -448,6 +451,7 @@ __global__ void __launch_bounds__(kChunkThreads, 1) cache_chunk_kernel(const Cac
       const int32_t* table = a.table + b * a.table_stride + c0;
       bool ok = true;
       int issued = 0;
+      int unit = 0, before = 0;  // of the value scales: the last page's, and the last 32 pages' by lane
       for (int base = 0; base < P && ok; base += 32) {
         // 32 pages' numbers and scales at once; -1 and 0: not there
         int pg = -1;
@@ -482,6 +486,12 @@ __global__ void __launch_bounds__(kChunkThreads, 1) cache_chunk_kernel(const Cac
         // the first pages' copies go out before their scales have come
         const int ahead = base == 0 ? min(kRaw, P) : 0;
         for (int i = 0; i < ahead; ++i) issue(i, __shfl_sync(0xffffffffu, pg, i));
+        const int mine = page_units(vs, unit, lane);
+        int from = __shfl_sync(0xffffffffu, lane < 31 ? mine : before, (lane + 31) & 31);
+        if (base == 0 && lane == 0) from = mine;
+        const float turn = unit_turn(from, mine);
+        before = mine;
+        const PageScale ps = page_scale(a, ks, vs * unit_inverse(mine));
         for (int i = 0; i < min(32, P - base) && ok; ++i) {
           const int p = base + i, s = p % kRaw;
           const int page = __shfl_sync(0xffffffffu, pg, i);
@@ -490,11 +500,12 @@ __global__ void __launch_bounds__(kChunkThreads, 1) cache_chunk_kernel(const Cac
             if (!ok) break;
             issue(p, page);
           }
-          const float2 kv = make_float2(__shfl_sync(0xffffffffu, ks, i), __shfl_sync(0xffffffffu, vs, i));
-          if (lane == 0) {
+          if (lane == i) {
             // the scales' slot held page p - 8: page p - 2 has been converted, so the QK of page p - 6 is
             // complete, and it was issued behind P of page p - 8 in both tiles
-            sm.info[p % kInfo] = kv;
+            sm.info[p % kInfo] = make_float4(ps.ck, ps.ev, ps.vinv, turn != 1.f ? NAN : kSlack);
+            sm.turn[p % kInfo] = turn;
+            sm.unit = mine;
             mbar_arrive(&sm.raw_full[s]);
           }
           __syncwarp();
@@ -547,7 +558,7 @@ __global__ void __launch_bounds__(kChunkThreads, 1) cache_chunk_kernel(const Cac
       store(w, sm.k[kst] + (p & 1) * kPage * 128, kTileKeys);
 #pragma unroll
       for (int i = 0; i < PASSES; ++i) w[i] = *reinterpret_cast<const uint4*>(sm.raw[rs][1] + at + i * ROWS * D);
-      const int rows_in = sm.info[p % kInfo].y == 0.f ? 0 : ex.len - (c0 + p) * kPage;
+      const int rows_in = sm.info[p % kInfo].y == -INFINITY ? 0 : ex.len - (c0 + p) * kPage;
       fence_proxy_async_smem();
       __syncwarp();
       if (lane == 0) {
@@ -606,14 +617,14 @@ __global__ void __launch_bounds__(kChunkThreads, 1) cache_chunk_kernel(const Cac
             colO = tmem + 256 + x * 128 + lane_sel;
           }
         }
-        const float2 kv = sm.info[p % kInfo];
-        const PageScale ps = page_scale(a, kv.x, kv.y);
+        const float4 info = sm.info[p % kInfo];
+        const PageScale ps{info.x, info.y, info.z};
         const uint32_t col = colS + (p & 1) * 64;
         uint32_t sv[64], pw[32];
         tmem_ld32x2_wait(col, col + 32, sv);
         const int key0 = (c0 + p) * kPage;
-        if (key0 + kPage > lim_warp || kv.y == 0.f) {  // kv.y = 0: a page that is not there
-          const int end = kv.y == 0.f ? key0 : lim;
+        if (key0 + kPage > lim_warp || ps.ev == -INFINITY) {  // -inf: a page that is not there
+          const int end = ps.ev == -INFINITY ? key0 : lim;
 #pragma unroll
           for (int i = 0; i < 64; ++i)
             if (key0 + i >= end) sv[i] = 0xff800000u;
@@ -629,22 +640,24 @@ __global__ void __launch_bounds__(kChunkThreads, 1) cache_chunk_kernel(const Cac
           const float tm = fmaf(page_max(sv), c, ps.ev);
           if (tm > -INFINITY) m = ceilf(tm);
         }
-        float sum;
+        float sum, slack = info.w;
         while (true) {
           sum = page_weights<kPolyEvery>(sv, c, page_addend(ps, m), pw);
           const float mx = page_max(sv);
-          const float tm = mx == -INFINITY ? -INFINITY : fmaf(mx, c, ps.ev);
-          if (!__any_sync(0xffffffffu, tm > m + kSlack)) break;
+          const float tm = fmaxf(fmaf(mx, c, ps.ev), -INFINITY);  // NaN raises nothing
+          if (__all_sync(0xffffffffu, tm <= m + slack)) break;
           const float up = tm > m + kSlack ? ceilf(tm) : m;
           const float k = up == m || m == -INFINITY ? 1.f : ex2_approx(m - up);
           if (p > 0) {  // O follows, once the PV of the page before is complete
             ok = chunk_wait<1>(&sm.pv_done[x][(p - 1) & 1], ((p - 1) >> 1) & 1, abort_flag, st, kSiteCPv, blockIdx.x);
             if (!ok) break;
             tc_fence_after();
-            scale_o<D>(colO, k);
+            // and to the page's unit of value scales
+            scale_o<D>(colO, slack == kSlack ? k : k * sm.turn[p % kInfo]);
           }
           l *= k;
           m = up;
+          slack = kSlack;
         }
         if (!ok) break;
         l = fmaf(sum, ps.vinv, l);
@@ -665,7 +678,8 @@ __global__ void __launch_bounds__(kChunkThreads, 1) cache_chunk_kernel(const Cac
         // quarter of the Q tile (its last QK is complete, or there was none) 64
         // columns at a time, so that the stores run along rows, a few lines each.
         const bool part = a.splits > 1;
-        const float inv = part ? 1.f : (l != 0.f ? 1.f / l : 0.f);
+        const int unit = sm.unit;
+        const float inv = part ? 1.f : (l != 0.f ? __int_as_float(unit << 23) / l : 0.f);
         const long long pr = partial_row(a, b, h, qi, split);
         uint16_t* dst = a.out + b * a.ost.b + h * a.ost.h + static_cast<long long>(qi) * a.ost.n;
         uint8_t* stage = sm.q[x] + wq * 32 * D * 2;  // 8 KB (D = 128) or 4 KB
@@ -700,7 +714,7 @@ __global__ void __launch_bounds__(kChunkThreads, 1) cache_chunk_kernel(const Cac
           else store_rows<COLS / 8>(a, stage, b, hk, r - lane, rows, half, split, lane);
         }
         if (there) {
-          if (part) a.part_ml[pr] = make_float2(m, l);
+          if (part) a.part_ml[pr] = make_float2(m + static_cast<float>(unit - 127), l * unit_inverse(unit));
           else if (a.lse)
             a.lse[(static_cast<long long>(b) * a.H + h) * a.N + qi] =
                 l == 0.f ? -INFINITY : (m - kPBias + log2f(l)) * kLn2C;

@@ -15,11 +15,22 @@
 // 1 / vs on the page's sum.
 //
 // P is rounded to fp16 for the value product (11 bits against bf16's 8, and
-// e4m3 is exact in fp16); 2^kPBias lifts the range so that weights 2^-29 of the
-// row's largest are still held, and the lazy reference (raised only when a
-// row's maximum passes it by kSlack) keeps P at 2^15 at most. Queries are scaled
-// by a power of two per row before they are rounded to fp16: exact for fp16
-// inputs, and for bf16 inputs down to 2^-23 of the row's largest element.
+// e4m3 is exact in fp16); 2^kPBias lifts the range and the lazy reference (raised
+// only when a row's maximum passes it by kSlack) keeps P at 2^15 at most, so
+// that P down to 2^-29 of the row's largest is held. P is a weight times a value
+// scale: were that scale the page's as it is, one page with a large value (2^29
+// times its neighbours') would push the others' P out of fp16 even for rows and
+// columns in which that page holds nothing. So value scales are taken relative
+// to a unit, vs / U, and where a page's differs from U by more than 2^kUnitSlack,
+// U becomes that page's scale and O, which is in fp32, is brought to it (rare:
+// pages of one head differ by less; the warp that fetches the pages works the
+// units out: 1,213 us for 8 heads x 3,600 queries x 75,600 keys, 1,218 without).
+// With all scales within 2^kUnitSlack of U, weights down to 2^-17 of the row's
+// largest are held whatever the scales are, down to 2^-29 where they are equal.
+//
+// Queries are scaled by a power of two per row before they are rounded to fp16:
+// exact for fp16 inputs, and for bf16 inputs down to 2^-23 of the row's largest
+// element.
 #pragma once
 
 #include <cuda_bf16.h>
@@ -37,6 +48,7 @@ namespace {
 constexpr int kPage = 64;
 constexpr float kPBias = 5.f;
 constexpr float kSlack = 10.f;
+constexpr int kUnitSlack = 6;
 constexpr float kLog2eC = 1.4426950408889634f;
 constexpr float kLn2C = 0.6931471805599453f;
 constexpr unsigned int kErrPage = 9;  // == SOLATTN_ERR_PAGE
@@ -160,8 +172,33 @@ __device__ __forceinline__ void row_factor(float amax, float* mul, float* inv) {
   *inv = __int_as_float((127 + e - 9) << 23);
 }
 
-// What a page's scores and weights are multiplied by, from its scales; vs = 0
-// stands for a page that is not there, whose tokens then weigh nothing.
+// Units of the value scales of 32 pages, lane i having page i's scale (0: not
+// there): the biased exponent of a power of two, from `unit`, that of the page
+// before (0: there was none), which becomes the last page's. Warp-collective.
+__device__ __forceinline__ int page_units(float vs, int& unit, int lane) {
+  const int x = (__float_as_int(vs) >> 23) & 255;
+  const bool known = x != 0 && x < 254;  // neither infinite nor NaN
+  const unsigned int m = __ballot_sync(0xffffffffu, known);
+  if (unit == 0 && m) unit = __shfl_sync(0xffffffffu, x, __ffs(m) - 1);
+  int mine = unit;
+  unsigned int far = __ballot_sync(0xffffffffu, known && abs(x - unit) > kUnitSlack);
+  while (far) {  // rare
+    const int first = __ffs(far) - 1;
+    unit = __shfl_sync(0xffffffffu, x, first);
+    if (lane >= first) mine = unit;
+    far = __ballot_sync(0xffffffffu, known && lane > first && abs(x - unit) > kUnitSlack);
+  }
+  return mine;
+}
+// 2^(from - to) of two units: what O is multiplied by when the unit changes.
+__device__ __forceinline__ float unit_turn(int from, int to) {
+  return __int_as_float((127 + min(max(from - to, -126), 126)) << 23);
+}
+__device__ __forceinline__ float unit_inverse(int unit) { return __int_as_float((254 - unit) << 23); }
+
+// What a page's scores and weights are multiplied by, from its scales, that of
+// the values in their unit; vs = 0 stands for a page that is not there, whose
+// tokens then weigh nothing.
 struct PageScale {
   float ck;    // ks * scale * log2(e)
   float ev;    // log2(vs)

@@ -59,7 +59,9 @@ struct __align__(1024) StepSmem {
     };
   };
   uint4 q[D / 16][32];    // Q fragments of step j, by lane
-  float2 scale[kStages];  // of keys and values; 0 values: the page is not there
+  float2 scale[kStages];  // of keys, and of values in their unit; 0 values: the page is not there
+  float turn[kStages];    // what a warp's O is multiplied by before the page
+  int unit[kWarps];       // of each warp's last page
   uint64_t full[kStages], empty[kStages];
   int nan;  // a value that only some rows see is NaN
   int abort_flag;
@@ -92,6 +94,7 @@ __global__ void __launch_bounds__((kWarps + 1) * 32, 3)
       mbar_init(&sm.full[i], 2);  // the copies' issue and the scales
       mbar_init(&sm.empty[i], 2);  // two warps share a page
     }
+    for (int i = 0; i < kWarps; ++i) sm.unit[i] = 127;
     sm.nan = 0;
     sm.abort_flag = 0;
     fence_barrier_init();
@@ -122,6 +125,7 @@ __global__ void __launch_bounds__((kWarps + 1) * 32, 3)
     }
     bool ok = true;
     int issued = 0;
+    int unit = 0, before = 0;  // of the value scales: the last page's, and the last 32 pages' by lane
     for (int base = c0; base < c1 && ok; base += 32) {
       // 32 pages' numbers and scales at once
       int pg = -1;
@@ -139,36 +143,45 @@ __global__ void __launch_bounds__((kWarps + 1) * 32, 3)
       const int count = min(32, c1 - base);
       // the first pages' copies go out before their scales have come
       const int ahead = base == c0 ? min(count, ST) : 0;
-      auto issue = [&](int n, int page) {
+      auto issue = [&](int n, int page) {  // by one lane
 #ifdef SOLATTN_TEST_HOOKS
         if (n == 0 && static_cast<int>(blockIdx.x) == g_hook_skip_cta) return;  // this page never arrives
 #endif
-        if (lane == 0) {
-          const int s = n % ST;
-          if (page >= 0) {
-            mbar_arrive_expect_tx(&sm.full[s], 2 * kPage * D);
-            tma_load_4d(sm.k[s], &tmK, &sm.full[s], 0, 0, hk, page);
-            tma_load_4d(sm.v[s], &tmV, &sm.full[s], 0, 0, hk, page);
-          } else {
-            mbar_arrive(&sm.full[s]);
-          }
+        const int s = n % ST;
+        if (page >= 0) {
+          mbar_arrive_expect_tx(&sm.full[s], 2 * kPage * D);
+          tma_load_4d(sm.k[s], &tmK, &sm.full[s], 0, 0, hk, page);
+          tma_load_4d(sm.v[s], &tmV, &sm.full[s], 0, 0, hk, page);
+        } else {
+          mbar_arrive(&sm.full[s]);
         }
-        issued = n + 1;
       };
-      for (int i = 0; i < ahead; ++i) issue(i, __shfl_sync(0xffffffffu, pg, i));
+      if (lane < ahead) issue(lane, pg);
+      __syncwarp();
+      issued = max(issued, ahead);
+      const int mine = page_units(vs, unit, lane);
+      vs *= unit_inverse(mine);
+      // a warp's page before this one is the last but one
+      int from = __shfl_sync(0xffffffffu, lane < 30 ? mine : before, (lane + 30) & 31);
+      if (base == c0 && lane < 2) from = mine;
+      const float turn = unit_turn(from, mine);
+      before = mine;
+#pragma unroll 1
       for (int i = 0; i < count && ok; ++i) {
         const int n = base + i - c0, s = n % ST;
-        const int page = __shfl_sync(0xffffffffu, pg, i);
         if (i >= ahead) {
           if (n >= ST)
             ok = __all_sync(0xffffffffu, mbar_wait(&sm.empty[s], ((n / ST) & 1) ^ 1, abort_flag, st, kSiteStepEmpty,
                                                    blockIdx.x));
           if (!ok) break;
-          issue(n, page);
+          if (lane == i) issue(n, pg);
+          issued = n + 1;
         }
-        const float2 kv = make_float2(__shfl_sync(0xffffffffu, ks, i), __shfl_sync(0xffffffffu, vs, i));
-        if (lane == 0) {
-          sm.scale[s] = kv;
+        if (lane == i) {
+          sm.scale[s] = make_float2(ks, vs);
+          sm.turn[s] = turn;
+          sm.unit[2 * (n & 1)] = mine;
+          if ((c0 + n) * kPage + 32 < seen) sm.unit[2 * (n & 1) + 1] = mine;  // its warp has rows that see it
           mbar_arrive(&sm.full[s]);
         }
       }
@@ -283,7 +296,7 @@ __global__ void __launch_bounds__((kWarps + 1) * 32, 3)
             if (base + 16 * (nt / 2) + tok[2 * (nt & 1) + (e & 1)] >= lim[e >> 1]) sc[nt][e] = -INFINITY;
       }
       float mx[2];
-      bool raise = false;
+      bool raise = sm.turn[s] != 1.f;
 #pragma unroll
       for (int x = 0; x < 2; ++x) {
         mx[x] = -INFINITY;
@@ -298,11 +311,12 @@ __global__ void __launch_bounds__((kWarps + 1) * 32, 3)
         for (int x = 0; x < 2; ++x) {
           const float mn = mx[x] > m[x] + kSlack ? ceilf(mx[x]) : m[x];
           const float k = m[x] == mn ? 1.f : ex2_approx(m[x] - mn);  // 0 from -inf
+          const float ko = k * sm.turn[s];  // and to the page's unit of value scales
           l[x] *= k;
 #pragma unroll
           for (int j = 0; j < D / 8; ++j) {
-            o[j][2 * x] *= k;
-            o[j][2 * x + 1] *= k;
+            o[j][2 * x] *= ko;
+            o[j][2 * x + 1] *= ko;
           }
           m[x] = mn;
         }
@@ -376,14 +390,15 @@ __global__ void __launch_bounds__((kWarps + 1) * 32, 3)
 
   // ---- the four warps' results joined, over the ring (every copy has landed and been read)
   named_bar_sync(1, kWarps * 32);
+  const int unit = sm.unit[warp];  // references and sums without it
 #pragma unroll
   for (int x = 0; x < 2; ++x) {
     l[x] += __shfl_xor_sync(0xffffffffu, l[x], 1);
     l[x] += __shfl_xor_sync(0xffffffffu, l[x], 2);
     const int r = g + 8 * x;
     if (t == 0) {
-      sm.m[warp][r] = m[x];
-      sm.l[warp][r] = l[x];
+      sm.m[warp][r] = m[x] + static_cast<float>(unit - 127);
+      sm.l[warp][r] = l[x] * unit_inverse(unit);
     }
     // column of value tile j and accumulator e: tile's byte j of the lanes' runs
 #pragma unroll

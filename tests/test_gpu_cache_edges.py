@@ -58,3 +58,95 @@ def test_tiles_that_see_no_page(d, dtype):
                 assert (out[b, :, :blind] == 0).all() and (lse[b, :, :blind] == -math.inf).all()
                 assert (out[b, :, blind:] > 0).all() and torch.isfinite(lse[b, :, blind:]).all()
     assert sa.status(ws) == 0
+
+
+def _cache_of(k, v, seed):
+    """A cache that holds k and v [heads, n, d] (fp32) in scattered pages, and its table; scales by the append's rule."""
+    H, n, d = k.shape
+    columns = (n + 63) // 64
+    c = sa.Cache.empty(columns + 2, H, d)
+    t = torch.randperm(columns + 2, generator=_gen(seed))[:columns].view(1, columns).to(torch.int32).cuda()
+    sa.cache_append(c, k[None].cuda(), v[None].cuda(), t, _i32([0]))
+    return c, t
+
+
+def _held(x8, scale, t, h, n):
+    """fp64 [n, d] of what head h of the cache holds."""
+    p = t[0].long().cpu()
+    return (x8.cpu()[p, h].double() * scale.cpu()[p, h].double()[:, None, None]).flatten(0, 1)[:n]
+
+
+COPIES = 222  # sequences with the same pages and queries: enough of them that no key axis is split
+
+
+def _attend_and_check(q, c, t, n, causal):
+    """A call of many equal sequences: the same bits for each, and 64-bit attention on the held values. The bounds are
+    those of the weights' rounding (2^-11 of a weight), of scores (delta = 2^-18 sum |q||k| scale), of sums and
+    exponentials (2^-15); and what a weight below fp16's normal range loses, 2^-25 in units where the row's largest is
+    2^4 at least. Those units hold weight times value scale, each scale within 2^6 of the unit that follows them, so of
+    every value that a row sees at most 2^-25 2^-4 2^6 2^6 |v|."""
+    _, H, N, d = q.shape
+    out, lse = sa.cache_attention(q.expand(COPIES, H, N, d), c, t.repeat(COPIES, 1), _i32([n] * COPIES), causal=causal,
+                                  out=torch.empty((COPIES, H, N, d), dtype=q.dtype, device="cuda"))
+    assert torch.equal(out, out[:1].expand_as(out)) and torch.equal(lse, lse[:1].expand_as(lse))
+    eps = torch.finfo(q.dtype).eps
+    for h in range(H):
+        j = h // (H // c.heads)
+        k, v = _held(c.k, c.k_scale, t, j, n), _held(c.v, c.v_scale, t, j, n)
+        o, l, mag, size = ref.attend(q[0, h].cpu(), k, v, causal, N, d ** -0.5)
+        total = v.abs().cumsum(0)
+        total = torch.stack([total[max(0, n - N + i) if causal else n - 1] for i in range(N)])
+        delta = 2.0 ** -18 * size[:, None]
+        tol = (2.0 ** -11 + 2.0 ** -15 + 2 * delta) * mag + 2.0 ** -17 * total + eps / 2 * 1.01 * o.abs()
+        err = (out[0, h].cpu().double() - o).abs()
+        assert (err <= tol).all(), (h, float((err / tol.clamp(min=1e-30)).max()))
+        e2 = (lse[0, h].cpu().double() - l).abs()
+        assert (e2 <= delta[:, 0] + 2.0 ** -15 + 2.0 ** -22 * l.abs()).all()
+
+
+OUTLIERS = [
+    # tokens, (token, column, value) of the outliers
+    (128, [(127, 5, 1e9)]),                        # the second page's last token
+    (500, [(200, 0, 1e9), (201, 63, -3e8)]),       # pages of ordinary size before and behind
+    (700, [(0, 1, 1e12), (699, 2, 1e12)]),         # the first and the last page
+    (900, [(64 * i + 9, i, 10.0 ** (i % 5 * 3)) for i in range(14)]),  # every page another size
+]
+
+
+@pytest.mark.parametrize("d", [64, 128])
+@pytest.mark.parametrize("N", [2, 60, 140])
+@pytest.mark.parametrize("n,outliers", OUTLIERS)
+def test_one_large_value_leaves_other_tokens_and_columns_alone(n, outliers, N, d):
+    """Values with an outlier in one column: its page's scale rises until the page's other values are 0, and the rows in
+    front of it and every other column still have the other pages' values to full accuracy."""
+    if N > n:
+        pytest.skip("more queries than tokens")
+    H = 2
+    k, v = (torch.randn((H, n, d), generator=_gen(i + n)) for i in range(2))
+    for token, column, value in outliers:
+        v[:, token, column] = value
+    c, t = _cache_of(k, v, seed=n)
+    q = torch.randn((1, 2 * H, N, d), generator=_gen(N)).to(torch.bfloat16).cuda()
+    for causal in (True, False):
+        _attend_and_check(q, c, t, n, causal)
+
+
+@pytest.mark.parametrize("d", [64, 128])
+@pytest.mark.parametrize("N", [1, 30, 100])
+def test_value_scales_over_the_whole_range(N, d):
+    """Pages' value scales from 2^-32 to 2^32 in any order, zero pages among them; a whole column that only the smallest
+    page fills comes out accurately."""
+    n, H = 64 * 9, 1
+    k, v = (torch.randn((H, n, d), generator=_gen(i + 77)) for i in range(2))
+    exponents = [-32, 32, -32, 0, 31, -9, 12, -20, 4]
+    v = v.view(H, 9, 64, d)
+    for i, e in enumerate(exponents):
+        v[:, i] = (v[:, i] / v[:, i].abs().amax()) * 440.0 * 2.0 ** e
+        v[:, i, :, 7] *= i == 2
+    v[:, 6] = 0
+    c, t = _cache_of(k, v.view(H, n, d), seed=3)
+    held = c.v_scale[t[0].long()]
+    assert float(held.min()) == 2.0 ** -32 and float(held.max()) == 2.0 ** 32
+    q = torch.randn((1, 2, N, d), generator=_gen(N)).to(torch.bfloat16).cuda()
+    for causal in (True, False):
+        _attend_and_check(q, c, t, n, causal)
