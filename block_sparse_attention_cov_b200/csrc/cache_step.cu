@@ -186,9 +186,12 @@ __global__ void __launch_bounds__((kWarps + 1) * 32, 3)
         }
       }
     }
-    if (!ok && lane == 0)  // teardown after a wait that gave up: issued copies land before the block exits
+    // every copy has landed before the ring is written over and before the block
+    // exits: a warp whose wait gave up has not seen its pages arrive
+    if (lane == 0)
       for (int n = max(0, issued - ST); n < issued; ++n) mbar_wait_quiet(&sm.full[n % ST], (n / ST) & 1);
     __syncwarp();
+    named_bar_sync(2, (kWarps + 1) * 32);
     __syncthreads();  // with the warps' results
     return;
   }
@@ -389,7 +392,7 @@ __global__ void __launch_bounds__((kWarps + 1) * 32, 3)
   }
 
   // ---- the four warps' results joined, over the ring (every copy has landed and been read)
-  named_bar_sync(1, kWarps * 32);
+  named_bar_sync(2, (kWarps + 1) * 32);
   const int unit = sm.unit[warp];  // references and sums without it
 #pragma unroll
   for (int x = 0; x < 2; ++x) {

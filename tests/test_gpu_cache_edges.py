@@ -150,3 +150,29 @@ def test_value_scales_over_the_whole_range(N, d):
     q = torch.randn((1, 2, N, d), generator=_gen(N)).to(torch.bfloat16).cuda()
     for causal in (True, False):
         _attend_and_check(q, c, t, n, causal)
+
+
+@pytest.mark.parametrize("d", [64, 128])
+@pytest.mark.parametrize("n", [1, 64, 200])
+def test_expired_waits_of_short_parts(n, d):
+    """Parts of at most four pages, all of whose copies are on their way before a wait is due: where the first page never
+    comes, every block ends with its other copies landed, and the next call gives its bits, time after time."""
+    B, H = 90, 2
+    k, v = (torch.randn((H, n, d), generator=_gen(i + n)) for i in range(2))
+    c, t = _cache_of(k, v, seed=n)
+    t = t.repeat(B, 1)
+    q = torch.randn((B, H, 2, d), generator=_gen(4)).to(torch.bfloat16).cuda()
+    lengths = _i32([n] * B)
+    ws = sa.cache_workspace(q, c, t)
+    want, want_lse = sa.cache_attention(q, c, t, lengths, ws=ws)
+    lib = _lib.lib()
+    for _ in range(3):
+        assert lib.solattn_test_set_hook(0, 20_000_000) == 0
+        try:
+            sa.cache_attention(q, c, t, lengths, ws=ws)
+            assert sa.status(ws) == _lib.ERR_TIMEOUT
+        finally:
+            assert lib.solattn_test_set_hook(-1, 2_000_000_000) == 0
+        ws[:_lib.WORKSPACE_BYTES].zero_()
+        out, lse = sa.cache_attention(q, c, t, lengths, ws=ws)
+        assert sa.status(ws) == 0 and torch.equal(out, want) and torch.equal(lse, want_lse)
