@@ -62,8 +62,8 @@ struct __align__(1024) ChunkSmem {
   uint8_t k[kKStages][kTileKeys * D * 2]; // the same
   uint8_t v[kVStages][kPage * D * 2];     // SW128 panels of 64 rows
   uint8_t raw[kRaw][2][kPage * D];        // keys and values of a page, e4m3
-  float4 info[kInfo];                     // a page's factors (PageScale), and kSlack: NaN where the unit changes
-  float turn[kInfo];                      // what O is multiplied by before the page
+  float4 info[kInfo];                     // a page's factors (PageScale), and kSlack: NaN where turn is not 1
+  float turn[kInfo];                      // what O is multiplied by before the page; NaN: a scale is NaN
   int unit;                               // of the last page, as its exponent
   uint64_t q_full[2], k_full[kKStages], k_empty[kKStages], v_full[kVStages], v_empty[kVStages];
   uint64_t raw_full[kRaw], raw_empty[kRaw];
@@ -492,6 +492,7 @@ __global__ void __launch_bounds__(kChunkThreads, 1) cache_chunk_kernel(const Cac
         const float turn = unit_turn(from, mine);
         before = mine;
         const PageScale ps = page_scale(a, ks, vs * unit_inverse(mine));
+        const bool no_number = isnan(ps.ck) || isnan(ps.ev);
         for (int i = 0; i < min(32, P - base) && ok; ++i) {
           const int p = base + i, s = p % kRaw;
           const int page = __shfl_sync(0xffffffffu, pg, i);
@@ -503,8 +504,9 @@ __global__ void __launch_bounds__(kChunkThreads, 1) cache_chunk_kernel(const Cac
           if (lane == i) {
             // the scales' slot held page p - 8: page p - 2 has been converted, so the QK of page p - 6 is
             // complete, and it was issued behind P of page p - 8 in both tiles
-            sm.info[p % kInfo] = make_float4(ps.ck, ps.ev, ps.vinv, turn != 1.f ? NAN : kSlack);
-            sm.turn[p % kInfo] = turn;
+            sm.info[p % kInfo] = no_number ? make_float4(0.f, 0.f, 1.f, NAN)
+                                           : make_float4(ps.ck, ps.ev, ps.vinv, turn != 1.f ? NAN : kSlack);
+            sm.turn[p % kInfo] = no_number ? NAN : turn;
             sm.unit = mine;
             mbar_arrive(&sm.raw_full[s]);
           }
@@ -648,14 +650,16 @@ __global__ void __launch_bounds__(kChunkThreads, 1) cache_chunk_kernel(const Cac
           if (__all_sync(0xffffffffu, tm <= m + slack)) break;
           const float up = tm > m + kSlack ? ceilf(tm) : m;
           const float k = up == m || m == -INFINITY ? 1.f : ex2_approx(m - up);
+          // the unit of the value scales that the page turns to; a page without a number for
+          // a scale makes the sums of the rows that see it NaN
+          const float turn = slack == kSlack ? 1.f : sm.turn[p % kInfo];
           if (p > 0) {  // O follows, once the PV of the page before is complete
             ok = chunk_wait<1>(&sm.pv_done[x][(p - 1) & 1], ((p - 1) >> 1) & 1, abort_flag, st, kSiteCPv, blockIdx.x);
             if (!ok) break;
             tc_fence_after();
-            // and to the page's unit of value scales
-            scale_o<D>(colO, slack == kSlack ? k : k * sm.turn[p % kInfo]);
+            scale_o<D>(colO, isnan(turn) ? k : k * turn);
           }
-          l *= k;
+          l *= isnan(turn) && lim > key0 ? NAN : k;
           m = up;
           slack = kSlack;
         }

@@ -333,8 +333,9 @@ __global__ void __launch_bounds__((kWarps + 1) * 32, 3)
           sc[nt][e] = ex2_approx(sc[nt][e] + sub[e >> 1]);
           sum[e >> 1] += sc[nt][e];
         }
-      l[0] = fmaf(sum[0], ps.vinv, l[0]);
-      l[1] = fmaf(sum[1], ps.vinv, l[1]);
+      // a row that sees nothing of the page is not touched by its scale, NaN or not
+      l[0] = sum[0] == 0.f ? l[0] : fmaf(sum[0], ps.vinv, l[0]);
+      l[1] = sum[1] == 0.f ? l[1] : fmaf(sum[1], ps.vinv, l[1]);
 #pragma unroll
       for (int grp = 0; grp < 2; ++grp) {
         uint32_t vw[4][D / 32];

@@ -176,3 +176,24 @@ def test_expired_waits_of_short_parts(n, d):
         ws[:_lib.WORKSPACE_BYTES].zero_()
         out, lse = sa.cache_attention(q, c, t, lengths, ws=ws)
         assert sa.status(ws) == 0 and torch.equal(out, want) and torch.equal(lse, want_lse)
+
+
+@pytest.mark.parametrize("which", ["k_scale", "v_scale"])
+@pytest.mark.parametrize("N", [1, 20, 150])
+def test_scale_that_is_no_number(N, which):
+    """A page whose scale is NaN gives NaN in the rows that see one of its tokens, in either kernel, and leaves the other
+    rows' bits alone."""
+    n, H, d = 320, 1, 128
+    k, v = (torch.randn((H, n, d), generator=_gen(i + 5)) for i in range(2))
+    c, t = _cache_of(k, v, seed=8)
+    q = torch.randn((1, 2, N, d), generator=_gen(N)).to(torch.bfloat16).cuda()
+    for causal in (True, False):
+        clean, clean_lse = sa.cache_attention(q, c, t, _i32([n]), causal=causal)
+        page = int(t[0, 4])  # tokens 256 .. 319
+        old = float(getattr(c, which)[page, 0])
+        getattr(c, which)[page, 0] = math.nan
+        out, lse = sa.cache_attention(q, c, t, _i32([n]), causal=causal)
+        getattr(c, which)[page, 0] = old
+        blind = max(0, N - 64) if causal else 0
+        assert torch.equal(out[:, :, :blind], clean[:, :, :blind]) and torch.equal(lse[:, :, :blind], clean_lse[:, :, :blind])
+        assert torch.isnan(out[:, :, blind:]).all() and torch.isnan(lse[:, :, blind:]).all()
