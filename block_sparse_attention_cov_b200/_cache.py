@@ -36,6 +36,8 @@ class Cache:
             raise ValueError("a page must be contiguous [heads, 64, d]")
         if heads > 1 and k_scale.stride(1) != 1:
             raise ValueError("a page's scales must be adjacent")
+        if pages > 1 and (k.stride(0) < heads * inner[0] or k_scale.stride(0) < heads):
+            raise ValueError("pages, and their scales, must be apart (not expand()ed from one)")
         self.k, self.v, self.k_scale, self.v_scale = k, v, k_scale, v_scale
         self.pages, self.heads, self.d = int(pages), int(heads), int(d)
         many = pages > 1
