@@ -73,6 +73,8 @@ def _strides(t):
     if t.is_contiguous():
         return _lib.StridesStruct(0, 0, 0)
     sb, sh, sn, _ = t.stride()
+    if sb == sh == sn == 0:
+        raise ValueError("a tensor of one repeated row (expand()) is not supported")
     return _lib.StridesStruct(sb, sh, sn)
 
 

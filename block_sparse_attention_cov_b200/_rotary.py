@@ -136,4 +136,9 @@ def rotary_pool(q, k, v, rope: Rotary, positions, out=None, stats: PooledStats |
 
 def _shared_strides(t):
     """The strides as they are, for the calls that check every one of them."""
-    return None if t.is_contiguous() else _strides_struct(*t.stride()[:3])
+    if t.is_contiguous():
+        return None
+    strides = t.stride()[:3]
+    if not any(strides):
+        raise ValueError("a tensor of one repeated row (expand()) is not supported")
+    return _strides_struct(*strides)
