@@ -66,7 +66,7 @@ class Rotary:
         signed = [f - (1 << 64) if f >= 1 << 63 else f for f in freq]
         self.freq = torch.tensor(signed, dtype=torch.int64).to(device)  # the 64-bit words of solattn_rotary_t.freq
         self.axis = torch.tensor(list(axis), dtype=torch.int32).to(device)
-        self._layout, self._freq, self._axis = LAYOUTS[layout], self.freq.data_ptr(), self.axis.data_ptr()
+        self._layout = LAYOUTS[layout]
 
     def _struct(self, positions, B: int, N: int):
         """solattn_rotary_t for int32 positions [N], [B, N] (one axis) or [N, axes], [B, N, axes]."""
@@ -80,8 +80,9 @@ class Rotary:
         token = st[lead - 1] if N > 1 else 0
         if N > 1 and token < 1:
             raise ValueError("positions must not be one token's repeated (expand() along N)")
-        return _lib.RotaryStruct(self.rot, self._layout, self.axes, self.gain, self._freq, self._axis, positions.data_ptr(),
-                                 st[0] if lead == 2 and B > 1 else 0, token)
+        # the addresses as they are now: a copy of the object, or one whose tables moved, has other ones
+        return _lib.RotaryStruct(self.rot, self._layout, self.axes, self.gain, self.freq.data_ptr(), self.axis.data_ptr(),
+                                 positions.data_ptr(), st[0] if lead == 2 and B > 1 else 0, token)
 
 
 def _outputs(q, k, out):
@@ -109,7 +110,7 @@ def rotary(q, k, rope: Rotary, positions, inverse: bool = False, out=None):
     if q.get_device() < 0:
         raise ValueError("expected CUDA tensors")
     q_out, k_out = _outputs(q, k, out)
-    dev = _device_index(q, k, q_out, k_out, rope.freq, positions)
+    dev = _device_index(q, k, q_out, k_out, rope.freq, rope.axis, positions)
     _call("solattn_rotary", _lib.lib().solattn_rotary, dev, q.data_ptr(), _at(k), q_out.data_ptr(), _at(k_out), dtype, B, H,
           Hk, N, d, _tensor_strides(q), None if k is None else _tensor_strides(k), _tensor_strides(q_out),
           None if k is None else _tensor_strides(k_out), rope._struct(positions, B, N), 1 if inverse else 0)
@@ -127,7 +128,7 @@ def rotary_pool(q, k, v, rope: Rotary, positions, out=None, stats: PooledStats |
     if q_out.stride() != k_out.stride():
         raise ValueError("the outputs must share their strides")
     stats = _pooled_stats(q, stats)
-    dev = _device_index(q, k, v, q_out, k_out, stats.buffer, rope.freq, positions)
+    dev = _device_index(q, k, v, q_out, k_out, stats.buffer, rope.freq, rope.axis, positions)
     _call("solattn_rotary_pool", _lib.lib().solattn_rotary_pool, dev, q.data_ptr(), k.data_ptr(), v.data_ptr(),
           q_out.data_ptr(), k_out.data_ptr(), B, H, N, d, _shared_strides(q), _shared_strides(q_out),
           rope._struct(positions, B, N), stats.struct)

@@ -44,7 +44,7 @@ def test_tensors_of_one_row_repeated(call, monkeypatch):
     assert row.stride() == (0, 0, 0, 1)
     stats = sa.PooledStats(whole, None, (2, 3, 70, 64))
     rope = sa.Rotary.__new__(sa.Rotary)
-    rope.freq = whole
+    rope.freq = rope.axis = whole
     rope._struct = lambda *a: None
     with pytest.raises(ValueError, match="repeated row"):
         if call == "pool":
