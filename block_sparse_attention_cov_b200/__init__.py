@@ -153,30 +153,34 @@ def pooled_bytes(B: int, H: int, N: int, d: int) -> int:
 
 @dataclass
 class PooledStats:
-    """solattn_pool's outputs: one device buffer and fp32 views into it."""
+    """solattn_pool's outputs: one device buffer, the arrays' addresses in it, and views of them."""
 
     buffer: torch.Tensor
     struct: _lib.PooledStruct
     shape: tuple
 
+    def __setattr__(self, name, value):
+        if name == "buffer":  # with its views in other types
+            self.__dict__["_typed"] = None
+        self.__dict__[name] = value
+
     def view(self, name: str) -> torch.Tensor:
-        dtype, dims, strides, off = _pooled_view(self.shape, name)
-        whole = self.__dict__.get(dtype)
-        if whole is None:
-            whole = self.__dict__[dtype] = self.buffer.view(dtype)
-        return whole.as_strided(dims, strides, whole.storage_offset() + off)
+        size, dims, strides = _pooled_view(self.shape, name)
+        if self._typed is None:
+            self.__dict__["_typed"] = (self.buffer.view(torch.bfloat16), self.buffer.view(torch.float32))
+        whole = self._typed[size // 4]
+        off = getattr(self.struct, name) - self.buffer.data_ptr()
+        return whole.as_strided(dims, strides, whole.storage_offset() + off // size)
 
 
 @functools.lru_cache(maxsize=512)
 def _pooled_view(shape, name: str):
-    """(type, dimensions, strides, offset in elements) of an array of the pooled statistics."""
+    """(element bytes, dimensions, strides) of an array of the pooled statistics."""
     B, H, N, d = shape
     nb = (N + _lib.BLOCK - 1) // _lib.BLOCK
     dims = (B, H, d) if name == "kmean" else (B, H, d, d) if name == "kcov" else (B, H, nb, d)
     strides = (H * d, d, 1) if name == "kmean" else (H * dims[2] * d, dims[2] * d, d, 1)
-    dtype, size = (torch.bfloat16, 2) if name.endswith("16") else (torch.float32, 4)
-    offsets = dict(zip((n for n, _ in _lib.PooledStruct._fields_), _pooled_offsets(*shape)[1]))
-    return dtype, dims, strides, offsets[name] // size
+    return 2 if name.endswith("16") else 4, dims, strides
 
 
 @functools.lru_cache(maxsize=512)

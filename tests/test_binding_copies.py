@@ -29,3 +29,43 @@ def test_rotary_copies_point_at_their_own_frequencies(copied):
     rope.freq, rope.axis = rope.freq.clone(), rope.axis.clone()  # a move of the tables to other memory
     st = rope._struct(pos, 2, 5)
     assert st.freq == rope.freq.data_ptr() and st.axis == rope.axis.data_ptr()
+
+
+def _stats(B, H, N, d, lead=0):
+    """PooledStats over CPU memory whose arrays start `lead` bytes into the buffer."""
+    n, st = ctypes.c_size_t(0), _lib.PooledStruct()
+    buf = torch.empty(sa.pooled_bytes(B, H, N, d) + lead + 256, dtype=torch.uint8)
+    at = (buf.data_ptr() + 255) // 256 * 256 + lead
+    assert _lib.lib().solattn_pooled_layout(B, H, N, d, at, ctypes.byref(st), ctypes.byref(n)) == 0
+    return sa.PooledStats(buf, st, (B, H, N, d))
+
+
+ARRAYS = ("qbar", "kbar", "vbar", "kmean", "kcov", "kbar16", "vbar16")
+
+
+def test_pooled_views_follow_struct_and_buffer():
+    """A view is the memory that the C calls write: the struct's address, in the buffer held now."""
+    B, H, N, d = 2, 3, 200, 64
+    stats = _stats(B, H, N, d)
+    for turn in range(3):
+        for name in ARRAYS:
+            v = stats.view(name)
+            assert v.data_ptr() == getattr(stats.struct, name) and v.is_contiguous()
+            v.fill_(turn + 1)
+        assert all((stats.view(name) == turn + 1).all() for name in ARRAYS)
+        old = stats.buffer
+        other = _stats(B, H, N, d, lead=512 * (turn + 1))
+        stats.buffer, stats.struct = other.buffer, other.struct
+        assert all(stats.view(name).untyped_storage().data_ptr() == other.buffer.data_ptr() for name in ARRAYS)
+        assert not any(v is not stats.buffer and isinstance(v, torch.Tensor)
+                       and v.untyped_storage().data_ptr() == old.data_ptr() for v in vars(stats).values())
+    assert set(vars(stats)) >= {"buffer", "struct", "shape"} and all(isinstance(k, str) for k in vars(stats))
+
+
+def test_pooled_views_of_arrays_laid_out_by_the_caller():
+    """Arrays in another order than solattn_pooled_layout's."""
+    B, H, N, d = 1, 2, 64, 64
+    stats = _stats(B, H, N, d)
+    stats.struct.qbar, stats.struct.kbar = stats.struct.kbar, stats.struct.qbar
+    for name in ARRAYS:
+        assert stats.view(name).data_ptr() == getattr(stats.struct, name)
