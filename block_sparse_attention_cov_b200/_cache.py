@@ -16,7 +16,8 @@ __all__ = ["Cache", "cache_append", "cache_workspace", "cache_attention"]
 class Cache:
     """Pages of a cache: k, v float8_e4m3fn [pages, heads, 64, d] and float32 scales [pages, heads], the tensors that
     the calls read and write (any step between pages, as in a slice of a cache of several layers). A value is
-    k[p, h, t] * k_scale[p, h]. Cache.empty() makes them; which page holds what is the caller's table."""
+    k[p, h, t] * k_scale[p, h]. Cache.empty() makes them; which page holds what is the caller's table. The tensors are
+    written in place, never replaced: the calls use the addresses that they had when the Cache was made."""
 
     def __init__(self, k: torch.Tensor, v: torch.Tensor, k_scale: torch.Tensor, v_scale: torch.Tensor):
         for x in (k, v):
@@ -38,11 +39,19 @@ class Cache:
             raise ValueError("a page's scales must be adjacent")
         if pages > 1 and (k.stride(0) < heads * inner[0] or k_scale.stride(0) < heads):
             raise ValueError("pages, and their scales, must be apart (not expand()ed from one)")
-        self.k, self.v, self.k_scale, self.v_scale = k, v, k_scale, v_scale
+        self._tensors = (k, v, k_scale, v_scale)
         self.pages, self.heads, self.d = int(pages), int(heads), int(d)
         many = pages > 1
         self.struct = _lib.CacheStruct(k.data_ptr(), v.data_ptr(), k_scale.data_ptr(), v_scale.data_ptr(), pages, heads,
                                        d, k.stride(0) if many else 0, k_scale.stride(0) if many else 0)
+
+    k = property(lambda self: self._tensors[0])
+    v = property(lambda self: self._tensors[1])
+    k_scale = property(lambda self: self._tensors[2])
+    v_scale = property(lambda self: self._tensors[3])
+
+    def __reduce__(self):  # copies are made of the tensors, with their addresses
+        return Cache, self._tensors
 
     @classmethod
     def empty(cls, pages: int, heads: int, d: int, device=None) -> "Cache":

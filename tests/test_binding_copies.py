@@ -69,3 +69,33 @@ def test_pooled_views_of_arrays_laid_out_by_the_caller():
     stats.struct.qbar, stats.struct.kbar = stats.struct.kbar, stats.struct.qbar
     for name in ARRAYS:
         assert stats.view(name).data_ptr() == getattr(stats.struct, name)
+
+
+def _cache(monkeypatch, pages=3, heads=2, d=64):
+    """A Cache over CPU memory (its check for a device passed over)."""
+    from block_sparse_attention_cov_b200 import _cache
+    monkeypatch.setattr(torch.Tensor, "is_cuda", True)
+    monkeypatch.setattr(_cache, "_device_index", lambda *ts: 0)
+    k, v = (torch.zeros((pages, heads, 64, d), dtype=torch.uint8).view(torch.float8_e4m3fn) for _ in range(2))
+    return sa.Cache(k, v, torch.ones(pages, heads), torch.ones(pages, heads))
+
+
+def _points_at_its_own(c):
+    return (c.struct.k, c.struct.v, c.struct.k_scale, c.struct.v_scale) == \
+        tuple(x.data_ptr() for x in (c.k, c.v, c.k_scale, c.v_scale))
+
+
+@pytest.mark.parametrize("copied", [copy.copy, copy.deepcopy])
+def test_cache_copies_point_at_their_own_pages(copied, monkeypatch):
+    c = _cache(monkeypatch)
+    other = copied(c)
+    assert _points_at_its_own(c) and _points_at_its_own(other)
+    assert torch.equal(other.k_scale, c.k_scale) and (other.pages, other.heads, other.d) == (c.pages, c.heads, c.d)
+
+
+def test_cache_tensors_cannot_be_replaced_under_their_addresses(monkeypatch):
+    c = _cache(monkeypatch)
+    for name in ("k", "v", "k_scale", "v_scale"):
+        with pytest.raises(AttributeError):
+            setattr(c, name, getattr(c, name).clone())
+    assert _points_at_its_own(c)
