@@ -3,7 +3,6 @@ from __future__ import annotations
 
 import ctypes
 import functools
-import math
 
 import torch
 
@@ -138,8 +137,8 @@ def cache_attention(q, cache: Cache, table, lengths, counts=None, causal: bool =
     columns, step = _check_table(table, lengths, counts, B)
     if scale is None:
         scale = 0.0
-    elif not (math.isfinite(scale) and scale > 0):
-        raise ValueError("scale must be positive and finite")
+    elif not 0.0 < ctypes.c_float(scale).value < 2.0 ** 127:
+        raise ValueError("scale must be positive and below 2^127 in fp32")
     if out is None:
         out = torch.empty_like(q)
     elif out.shape != q.shape or out.dtype != q.dtype or out.stride(3) != 1:

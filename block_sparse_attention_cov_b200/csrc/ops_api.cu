@@ -286,7 +286,7 @@ int solattn_cache_attention(const void* q, int dtype, int B, int H, int N, int d
   int rc = check_attention_shape(B, H, N, d, cache->heads, columns);
   if (rc) return rc;
   if (!dtype_ok(dtype, false)) return SOLATTN_ERR_UNSUPPORTED;
-  if (cache->d != d || !(scale >= 0.f) || !std::isfinite(scale)) return SOLATTN_ERR_ARG;
+  if (cache->d != d || !(scale >= 0.f) || !(scale < 0x1p127f)) return SOLATTN_ERR_ARG;  // finite in log2 units too
   CacheView cv;
   if ((rc = check_cache(cache, table, columns, table_stride, lengths, counts, &cv))) return rc;
   if (!solattn::aligned16(q) || !solattn::aligned16(out) || !solattn::aligned4(lse)) return SOLATTN_ERR_ALIGN;

@@ -452,7 +452,7 @@ int solattn_cache_append(const void* k, const void* v, int dtype, int B, int N, 
  * and stand for the sequence's last counts[b] tokens. causal != 0: query i sees
  * keys 0 .. lengths[b] - counts[b] + i, else all lengths[b].
  *   out = softmax(scale q k^T) v  (q's type),  lse = ln of the sum (may be NULL)
- * scale 0 = 1/sqrt(d). A row that sees no key gets out 0 and lse -inf; rows
+ * scale 0 = 1/sqrt(d), else below 2^127. A row that sees no key gets out 0 and lse -inf; rows
  * i >= counts[b] of out and lse stay as they were. Strides of q and out are
  * multiples of 8 elements. workspace: solattn_cache_workspace_bytes(same sizes)
  * bytes, its status block cleared once, used by one call at a time; nothing else

@@ -1,11 +1,14 @@
 """Refusals by the binding for CUDA tensors, made as shapes and strides only (no device, no memory): what the kernels could
 not read or write in bounds is refused before its address is asked for."""
+import ctypes
+
 import pytest
 import torch
 from torch._subclasses.fake_tensor import FakeTensorMode
 
 import block_sparse_attention_cov_b200 as sa
 from block_sparse_attention_cov_b200 import _lib
+from block_sparse_attention_cov_b200.build import build
 
 E4M3 = torch.float8_e4m3fn
 
@@ -59,3 +62,21 @@ def test_tensors_of_one_row_repeated(call, monkeypatch):
             sa.rotary_pool(row, row, row, rope, whole, out=(whole, whole), stats=stats)
         else:
             sa.rotary_pool(whole, whole, whole, rope, whole, out=(row, row), stats=stats)
+
+
+@pytest.mark.parametrize("scale", [1e-50, 1e-46, 3e38, 1e39, 0.0, -1.0, float("nan"), float("inf")])
+def test_softmax_scales_that_are_none(scale):
+    """The C call takes the scale in fp32, where a tiny one becomes 0 (its word for the default) and a huge one infinite,
+    there or when it is brought to base 2."""
+    q, i = _empty(1, 2, 1, 64, dtype=torch.bfloat16), _empty(1, dtype=torch.int32)
+    cache = type("C", (), {"d": 64, "heads": 2, "k": q})()
+    with pytest.raises(ValueError, match="scale"):
+        sa.cache_attention(q, cache, _empty(1, 1, dtype=torch.int32), i, scale=scale)
+
+
+def test_softmax_scale_beyond_base_two_is_refused_by_the_library():
+    build()
+    fake, st = ctypes.c_void_p(0x7F0000000000), _lib.CacheStruct(*[0x7F0000000000] * 4, 4, 2, 64, 0, 0)
+    for scale, want in ((2.5e38, _lib.ERR_ARG), (float("inf"), _lib.ERR_ARG), (-1e-30, _lib.ERR_ARG)):
+        assert _lib.lib().solattn_cache_attention(fake, 0, 1, 4, 1, 64, None, st, fake, 2, 0, fake, None, 1, scale, fake, None,
+                                                  None, fake, 1 << 30, None) == want
