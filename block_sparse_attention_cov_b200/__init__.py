@@ -167,10 +167,9 @@ class PooledStats:
     def view(self, name: str) -> torch.Tensor:
         size, dims, strides = _pooled_view(self.shape, name)
         if self._typed is None:
-            self.__dict__["_typed"] = (self.buffer.view(torch.bfloat16), self.buffer.view(torch.float32))
-        whole = self._typed[size // 4]
-        off = getattr(self.struct, name) - self.buffer.data_ptr()
-        return whole.as_strided(dims, strides, whole.storage_offset() + off // size)
+            b = self.buffer
+            self.__dict__["_typed"] = (b.view(torch.bfloat16), b.view(torch.float32), b.untyped_storage().data_ptr())
+        return self._typed[size // 4].as_strided(dims, strides, (getattr(self.struct, name) - self._typed[2]) // size)
 
 
 @functools.lru_cache(maxsize=512)
