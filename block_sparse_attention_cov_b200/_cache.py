@@ -13,8 +13,8 @@ __all__ = ["Cache", "cache_append", "cache_workspace", "cache_attention"]
 
 
 class Cache:
-    """Pages of a cache: k, v float8_e4m3fn [pages, heads, 64, d] and float32 scales [pages, heads], the tensors that
-    the calls read and write (any step between pages, as in a slice of a cache of several layers). A value is
+    """Pages of a cache: k, v float8_e4m3fn [pages, heads, 64, d] and float32 scales [pages, heads] (2^-32 .. 2^32), the
+    tensors that the calls read and write (any step between pages, as in a slice of a cache of several layers). A value is
     k[p, h, t] * k_scale[p, h]. Cache.empty() makes them; which page holds what is the caller's table. The tensors are
     written in place, never replaced: the calls use the addresses that they had when the Cache was made."""
 
@@ -110,7 +110,8 @@ def _workspace_bytes(B: int, H: int, N: int, d: int, heads: int, columns: int) -
 
 
 def cache_workspace(q, cache: Cache, table) -> torch.Tensor:
-    """A workspace for cache_attention() of these sizes, its status cleared."""
+    """A workspace for cache_attention() of these sizes, its status cleared. Its bytes follow how the call is split and may
+    fall where a size grows: for calls of several sizes keep the largest of their workspaces."""
     B, H, N, d = q.shape
     ws = torch.empty(_workspace_bytes(B, H, N, d, cache.heads, table.shape[1]), dtype=torch.uint8, device=q.device)
     ws[:_lib.WORKSPACE_BYTES].zero_()
@@ -125,7 +126,8 @@ def cache_attention(q, cache: Cache, table, lengths, counts=None, causal: bool =
     among them; counts int32 [B] (None: N) of the N query rows are there and stand for the sequence's last tokens.
     causal: a query sees the keys up to its own place, else all of the sequence's. scale: 1/sqrt(d) when None. A row that
     sees no key gives 0 and -inf; rows behind counts[b] keep what out and lse held (torch.empty when allocated here).
-    ws: from cache_workspace(), kept by the caller for status(ws) and for graphs; allocated here when None."""
+    ws: from cache_workspace(), kept by the caller for status(ws) and for graphs; allocated here when None, and then
+    nobody learns of a page, length or count out of range (tokens of such a page are left out, lengths clamped)."""
     if q.dim() != 4 or q.stride(3) != 1:
         raise ValueError("q must be a [B, H, N, d] tensor with contiguous d")
     dtype = _dtype(q, _CODES16)

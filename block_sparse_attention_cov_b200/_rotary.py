@@ -22,7 +22,8 @@ class Rotary:
     rot: rotated leading elements of a head (even). layout: "half" (element p pairs with p + rot/2) or "interleaved"
     (2p with 2p + 1). sections: rotated pairs of each position axis (for video, t, h and w), each with frequencies
     theta^(-i / n) of its own; None: one axis. scaling: None, ("linear", factor), ("ntk", factor) or
-    ("yarn", factor, original_length[, fast, slow]). frequencies: rot / 2 values in radians per position that replace
+    ("yarn", factor, original_length[, fast, slow]), whose ramp is linear in a pair's turns within the original length
+    (for one linear in the pair's index give the frequencies and the gain). frequencies: rot / 2 values in radians per position that replace
     all of theta and scaling (pairs keep their axes)."""
 
     def __init__(self, rot: int, layout: str = "half", theta: float = 10000.0, sections=None, scaling=None,

@@ -298,7 +298,7 @@ template <typename Elem, int D>
 __global__ void __launch_bounds__(kChunkThreads, 1) cache_chunk_kernel(const CacheAttnArgs a, int tiles) {
   constexpr bool kPageSlots = D == 64;
   // At d = 64 both tiles' exponentials always meet: every eighth pair on the FMA
-  // pipe instead takes 256 x 8192 x 148 heads from 136 to 127 us (every fourth: 135
+  // pipe instead took 256 x 8192 x 148 heads from 136 to 127 us (every fourth: 135
   // us). At d = 128 they alternate, and the longer code costs (151 to 159 us).
   constexpr int kPolyEvery = D == 64 ? 8 : 0;
   extern __shared__ uint8_t smem_raw[];

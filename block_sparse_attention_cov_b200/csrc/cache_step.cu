@@ -198,7 +198,8 @@ __global__ void __launch_bounds__((kWarps + 1) * 32, 3)
 
   // ======================= four warps =======================
   // Q fragments of rows g and g + 8, scaled to fp16's range, in shared memory: in
-  // registers they would cost the third block of an SM
+  // registers they would cost the third block of an SM (all 128 a thread are taken,
+  // and at d = 128 one word spills)
   float rf[2];
   int lim[2];
 #pragma unroll

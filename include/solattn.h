@@ -351,7 +351,7 @@ typedef struct {
  *   SOLATTN_SCALING_NTK     theta becomes theta factor^(2n / (2n - 2))
  *   SOLATTN_SCALING_YARN    f (keep + (1 - keep) / factor), keep = clamp((r - slow) / (fast - slow), 0, 1),
  *                           r = original f / (2 pi) the turns within `original` tokens (usual: fast 32,
- *                           slow 1); gain 0.1 ln(factor) + 1
+ *                           slow 1); gain 0.1 ln(factor) + 1. The ramp is linear in r, not in i
  */
 enum solattn_rotary_scaling {
   SOLATTN_SCALING_NONE = 0,
@@ -395,7 +395,7 @@ int solattn_rotary_pool(const void* q, const void* k, const void* v, void* q_out
 /*
  * Key/value cache in 8 bits. A page holds 64 tokens of every head:
  *   k, v              e4m3 [pages][heads][64][d], d in {64, 128}
- *   k_scale, v_scale  fp32 [pages][heads], positive
+ *   k_scale, v_scale  fp32 [pages][heads], positive, 2^-32 .. 2^32
  * and a value is e4m3 * scale. page_stride (bytes, a multiple of 16) and
  * scale_stride (floats) are the steps between pages, 0 = contiguous. A sequence
  * is a row of a table [B][columns]: the page of each of its 64-token blocks
@@ -456,7 +456,9 @@ int solattn_cache_append(const void* k, const void* v, int dtype, int B, int N, 
  * i >= counts[b] of out and lse stay as they were. Strides of q and out are
  * multiples of 8 elements. workspace: solattn_cache_workspace_bytes(same sizes)
  * bytes, its status block cleared once, used by one call at a time; nothing else
- * in it is kept between calls. The same inputs give the same bits.
+ * in it is kept between calls. That size follows how the call is split: it may
+ * fall where a size grows, so a workspace for several sizes takes the largest of
+ * their bytes. A page's scale that is NaN gives NaN in the rows that see the page. The same inputs give the same bits.
  */
 int solattn_cache_workspace_bytes(int B, int H, int N, int d, int H_kv, int columns, size_t* bytes);
 int solattn_cache_attention(const void* q, int dtype, int B, int H, int N, int d, const solattn_strides_t* strides,
