@@ -80,14 +80,19 @@ COPIES = 222  # sequences with the same pages and queries: enough of them that n
 
 
 def _attend_and_check(q, c, t, n, causal):
+    for copies in (COPIES, 1):
+        _attend_copies(q, c, t, n, causal, copies)
+
+
+def _attend_copies(q, c, t, n, causal, copies):
     """A call of many equal sequences: the same bits for each, and 64-bit attention on the held values. The bounds are
     those of the weights' rounding (2^-11 of a weight), of scores (delta = 2^-18 sum |q||k| scale), of sums and
     exponentials (2^-15); and what a weight below fp16's normal range loses, 2^-25 in units where the row's largest is
     2^4 at least. Those units hold weight times value scale, each scale within 2^6 of the unit that follows them, so of
     every value that a row sees at most 2^-25 2^-4 2^6 2^6 |v|."""
     _, H, N, d = q.shape
-    out, lse = sa.cache_attention(q.expand(COPIES, H, N, d), c, t.repeat(COPIES, 1), _i32([n] * COPIES), causal=causal,
-                                  out=torch.empty((COPIES, H, N, d), dtype=q.dtype, device="cuda"))
+    out, lse = sa.cache_attention(q.expand(copies, H, N, d), c, t.repeat(copies, 1), _i32([n] * copies), causal=causal,
+                                  out=torch.empty((copies, H, N, d), dtype=q.dtype, device="cuda"))
     assert torch.equal(out, out[:1].expand_as(out)) and torch.equal(lse, lse[:1].expand_as(lse))
     eps = torch.finfo(q.dtype).eps
     for h in range(H):
@@ -110,6 +115,7 @@ OUTLIERS = [
     (500, [(200, 0, 1e9), (201, 63, -3e8)]),       # pages of ordinary size before and behind
     (700, [(0, 1, 1e12), (699, 2, 1e12)]),         # the first and the last page
     (900, [(64 * i + 9, i, 10.0 ** (i % 5 * 3)) for i in range(14)]),  # every page another size
+    (4500, [(64 * i + 7, i % 60, 1e9) for i in (0, 29, 31, 32, 33, 34, 40, 62, 63, 64, 66, 70)]),  # around 32 and 64 pages
 ]
 
 
